@@ -491,6 +491,109 @@ typedef struct moe_wq_params {
 size_t moe_wq_workspace_bytes(const moe_wq_params* p);
 moe_status moe_block_forward_wq(const moe_wq_params* p, void* stream);
 
+/* ------------------------------------------------------ MXFP8 and the norm
+ *
+ * MXFP8 (the OCP Microscaling elements): e4m3 values in groups of 32 along a
+ * row with one e8m0 scale byte c per group, standing for 2^(c - 127) (0xFF:
+ * NaN). Quantisation of a group: 2^j is the smallest power of two, j in
+ * [-127, 127], with amax / 2^j <= 448; the values are v / 2^j rounded to e4m3
+ * (nearest, ties to even). An all-zero group has c = 0; a group that holds an
+ * infinity or a NaN has c = 0xFF and reads back as 32 NaN.
+ *
+ * Activations: q [rows][K] e4m3, scale [rows][K/32] e8m0, row-major.
+ * Weights of G stacked [K, N] Linears, quantised along K:
+ *   q  [G][N][K] e4m3 (K contiguous);
+ *   sf [G][ceil(N/128)][ceil(K/128)][512] bytes: the scales of rows 128a ..
+ *      128a+127 and K range 128b .. 128b+127 form one 512-byte tile, row r,
+ *      group c (0..3) at byte 16*(r%32) + 4*(r%128/32) + c; rows past N and
+ *      groups past K hold 0.
+ */
+
+/*
+ * Residual addition, RMSNorm and MXFP8 output in one kernel: the seam between
+ * two sub-layers of the sandwich.
+ *   s = residual + (gamma_post x / sqrt(mean(x^2) + eps)  with gamma_post, else x)
+ *   y = gamma s / sqrt(mean(s^2) + eps)
+ * per row of [T, embed_dim], in fp32, each output rounded once from there:
+ *   sum = RNE_bf16(s), y = RNE_bf16(y), (q, scale) = MXFP8(y).
+ * residual, gamma_post and gamma (bf16; NULL: no addition, no post-norm, no
+ * learned scale) are optional, and so is each output, but one is needed and q
+ * comes with scale. embed_dim (0: MOE_EMBED_DIM) is a multiple of 8, of 32 with
+ * q, and at most 16384; eps 0 takes 1e-6. Rows are contiguous; x, residual, the
+ * gammas, sum, y, q 16-byte aligned. sum and y may each be the same buffer as x
+ * or as residual; any other overlap is refused.
+ */
+typedef struct moe_norm_params {
+  int T;
+  int embed_dim;
+  float eps;
+  const void* x;
+  const void* residual;
+  const void* gamma_post;
+  const void* gamma;
+  void* sum;
+  void* y;
+  void* q;
+  void* scale;
+} moe_norm_params;
+
+moe_status moe_add_rms_norm(const moe_norm_params* p, void* stream);
+
+typedef struct moe_mxfp8_linear {
+  const uint8_t* q;
+  const uint8_t* sf;
+} moe_mxfp8_linear;
+
+/* Sizes of q and sf for G stacked [K, N] Linears (K and N multiples of 64). */
+moe_status moe_mxfp8_weight_bytes(int groups, int K, int N, size_t* q_bytes, size_t* sf_bytes);
+
+/* Quantise bf16 weights w [groups][K][N] (N contiguous) into q and sf. */
+moe_status moe_mxfp8_quantize_weight(const void* w, int groups, int K, int N, uint8_t* q, uint8_t* sf, void* stream);
+
+/* Quantise rows x [rows][K] bf16 (K a multiple of 32) into q [rows][K], scale [rows][K/32]. */
+moe_status moe_mxfp8_quantize_act(const void* x, int rows, int K, uint8_t* q, uint8_t* scale, void* stream);
+
+/*
+ * One block with MXFP8 expert and shared Linears and MXFP8 activations:
+ *   h = MXFP8(gelu_tanh(x^ Wg) * (x^ Wu)) of the routed rows and of the shared
+ *   MLP, each from fp32, y = h Wd, out as in the bf16 block, with x^ the MXFP8
+ *   rows; products of 8-bit values, fp32 accumulation. The router reads x in
+ *   bf16 (top-k and weights as in the bf16 block).
+ * xq / xs (both or neither): the rows x already in MXFP8, e.g. as
+ * moe_add_rms_norm wrote them beside x; without them the call quantises x.
+ * Dims, w_router, router_bias, out, out_f32, idx_out, w_out, cnt_out as in
+ * moe_params; out may be NULL when out_f32 is given. Outputs must not overlap
+ * x, xq, xs or one another. workspace: at least moe_mxfp8_workspace_bytes(p),
+ * 256-byte aligned, or NULL for the library's cached allocation - but not while
+ * the stream is being captured, where NULL returns MOE_ERR_WORKSPACE (the
+ * cached allocation may be freed to grow while the graph still lives).
+ */
+typedef struct moe_mxfp8_params {
+  int T;
+  int top_k_experts;
+  int embed_dim;
+  int num_experts;
+  int expert_dim;
+  int hidden_dim;
+  const void* x;
+  const void* xq;
+  const void* xs;
+  const void* w_router;
+  const float* router_bias;
+  moe_mxfp8_linear wg, wu, wd; /* G = num_experts */
+  moe_mxfp8_linear sg, su, sd; /* G = 1 */
+  void* out;
+  float* out_f32;
+  int32_t* idx_out;
+  float* w_out;
+  int32_t* cnt_out;
+  void* workspace;
+  size_t workspace_bytes;
+} moe_mxfp8_params;
+
+size_t moe_mxfp8_workspace_bytes(const moe_mxfp8_params* p);
+moe_status moe_block_forward_mxfp8(const moe_mxfp8_params* p, void* stream);
+
 /* -------------------------------------------------------- dense GeGLU FFN
  *
  * The feed-forward of the dense E4B sibling (gm.nn.Gemma4_E4B

@@ -482,6 +482,73 @@ def moe_block_forward_wq(p: MoeWqParams, stream=None) -> int:
     return lib().moe_block_forward_wq(ctypes.byref(p), stream_handle(stream))
 
 
+# --------------------------------------------------- MXFP8 and the add-norm
+
+MXFP8_GROUP = 32
+
+
+class MoeNormParams(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("embed_dim", ctypes.c_int), ("eps", ctypes.c_float)] + [
+        (name, _vp) for name in ("x", "residual", "gamma_post", "gamma", "sum", "y", "q", "scale")
+    ]
+
+
+class MoeMxfp8Linear(ctypes.Structure):
+    _fields_ = [("q", _vp), ("sf", _vp)]
+
+
+class MoeMxfp8Params(ctypes.Structure):
+    _fields_ = (
+        [(name, ctypes.c_int) for name in ("T", "top_k_experts", "embed_dim", "num_experts", "expert_dim",
+                                           "hidden_dim")]
+        + [(name, _vp) for name in ("x", "xq", "xs", "w_router", "router_bias")]
+        + [(name, MoeMxfp8Linear) for name in ("wg", "wu", "wd", "sg", "su", "sd")]
+        + [(name, _vp) for name in ("out", "out_f32", "idx_out", "w_out", "cnt_out", "workspace")]
+        + [("workspace_bytes", ctypes.c_size_t)]
+    )
+
+
+EXPORTS.update(
+    {
+        "moe_add_rms_norm": (ctypes.c_int, [ctypes.POINTER(MoeNormParams), _vp]),
+        "moe_mxfp8_weight_bytes": (
+            ctypes.c_int,
+            [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(ctypes.c_size_t)],
+        ),
+        "moe_mxfp8_quantize_weight": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp]),
+        "moe_mxfp8_quantize_act": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp]),
+        "moe_mxfp8_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(MoeMxfp8Params)]),
+        "moe_block_forward_mxfp8": (ctypes.c_int, [ctypes.POINTER(MoeMxfp8Params), _vp]),
+    }
+)
+
+
+def moe_add_rms_norm(p: MoeNormParams, stream=None) -> int:
+    return lib().moe_add_rms_norm(ctypes.byref(p), stream_handle(stream))
+
+
+def moe_mxfp8_weight_bytes(groups: int, K: int, N: int) -> tuple[int, int]:
+    q, sf = ctypes.c_size_t(), ctypes.c_size_t()
+    check(lib().moe_mxfp8_weight_bytes(groups, K, N, ctypes.byref(q), ctypes.byref(sf)), "moe_mxfp8_weight_bytes")
+    return q.value, sf.value
+
+
+def moe_mxfp8_quantize_weight(w, groups, K, N, q, sf, stream=None) -> int:
+    return lib().moe_mxfp8_quantize_weight(ptr(w), groups, K, N, ptr(q), ptr(sf), stream_handle(stream))
+
+
+def moe_mxfp8_quantize_act(x, rows, K, q, scale, stream=None) -> int:
+    return lib().moe_mxfp8_quantize_act(ptr(x), rows, K, ptr(q), ptr(scale), stream_handle(stream))
+
+
+def moe_mxfp8_workspace_bytes(p: MoeMxfp8Params) -> int:
+    return lib().moe_mxfp8_workspace_bytes(ctypes.byref(p))
+
+
+def moe_block_forward_mxfp8(p: MoeMxfp8Params, stream=None) -> int:
+    return lib().moe_block_forward_mxfp8(ctypes.byref(p), stream_handle(stream))
+
+
 # ------------------------------------------------------------ dense GeGLU FFN
 
 E4B_EMBED_DIM = 2560

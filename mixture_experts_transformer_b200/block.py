@@ -301,6 +301,192 @@ def forward_wq(ww: WqWeights, x: torch.Tensor, *, top_k: int = B.TOP_K, router_b
     return res
 
 
+# --------------------------------------------------- MXFP8 and the add-norm
+
+
+def _rows(name: str, t: torch.Tensor, shape, dtypes, device) -> torch.Tensor:
+    """t itself, after checking that it is a contiguous [shape] tensor of one of `dtypes` on `device`."""
+    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: needs a contiguous {tuple(shape)} tensor of {' or '.join(map(str, dtypes))} on "
+                         f"{device}, got {tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
+    return t
+
+
+def _on_current_device(x: torch.Tensor) -> torch.device:
+    """x's device, which has to be the current one: the library launches there."""
+    if x.device.type != "cuda" or x.device.index != torch.cuda.current_device():
+        raise ValueError(f"x is on {x.device}: the library runs on the current CUDA device")
+    return x.device
+
+
+_BF16, _E4M3, _E8M0 = (torch.bfloat16,), (torch.float8_e4m3fn, torch.uint8), (torch.float8_e8m0fnu, torch.uint8)
+
+
+@dataclasses.dataclass
+class NormResult:
+    y: torch.Tensor | None
+    sum: torch.Tensor | None
+    q: torch.Tensor | None = None
+    scale: torch.Tensor | None = None
+
+
+def add_rms_norm(
+    x: torch.Tensor,
+    gamma: torch.Tensor | None = None,
+    *,
+    residual: torch.Tensor | None = None,
+    gamma_post: torch.Tensor | None = None,
+    quantize: bool = False,
+    y: torch.Tensor | None = None,
+    sum_out: torch.Tensor | None = None,
+    q: torch.Tensor | None = None,
+    scale: torch.Tensor | None = None,
+    eps: float = 1e-6,
+    stream=None,
+) -> NormResult:
+    """s = residual + (gamma_post-RMSNorm(x) with gamma_post, else x); y = gamma-RMSNorm(s), in one kernel.
+
+    x, residual [T, D] bf16; gamma, gamma_post [D] bf16. Returns y and sum = s
+    in bf16 and, with quantize=True or q and scale given, y in MXFP8: q [T, D]
+    e4m3 and scale [T, D/32] e8m0. Outputs may be passed in; y and sum_out may
+    each be x or residual itself (in place)."""
+    dev = _on_current_device(x)
+    T, D = x.shape
+    shape = (T, D)
+    _rows("x", x, shape, _BF16, dev)
+    for name, t, s in (("residual", residual, shape), ("gamma", gamma, (D,)), ("gamma_post", gamma_post, (D,)),
+                       ("y", y, shape), ("sum_out", sum_out, shape)):
+        if t is not None:
+            _rows(name, t, s, _BF16, dev)
+    y = torch.empty_like(x) if y is None else y
+    sum_out = torch.empty_like(x) if sum_out is None else sum_out
+    if quantize or q is not None or scale is not None:
+        q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev) if q is None else _rows("q", q, shape, _E4M3, dev)
+        sshape = (T, D // B.MXFP8_GROUP)
+        scale = (torch.empty(sshape, dtype=torch.float8_e8m0fnu, device=dev) if scale is None
+                 else _rows("scale", scale, sshape, _E8M0, dev))
+    p = B.MoeNormParams(T, D, eps, x.data_ptr(), B.ptr(residual), B.ptr(gamma_post), B.ptr(gamma), sum_out.data_ptr(),
+                        y.data_ptr(), B.ptr(q), B.ptr(scale))
+    B.check(B.moe_add_rms_norm(p, stream), "moe_add_rms_norm")
+    return NormResult(y, sum_out, q, scale)
+
+
+@dataclasses.dataclass
+class Mxfp8Linear:
+    """G stacked [K, N] Linears in MXFP8 on the device: codes [G, N, K] e4m3 and the scale tiles."""
+
+    q: torch.Tensor
+    sf: torch.Tensor
+    groups: int
+    K: int
+    N: int
+
+    def struct(self) -> B.MoeMxfp8Linear:
+        return B.MoeMxfp8Linear(self.q.data_ptr(), self.sf.data_ptr())
+
+
+def quantize_mxfp8_linear(w: torch.Tensor, stream=None) -> Mxfp8Linear:
+    """w [G, K, N] (or [K, N]) bf16 on the device -> MXFP8 along K (the library's quantiser)."""
+    w3 = w if w.dim() == 3 else w.unsqueeze(0)
+    G, K, N = w3.shape
+    _rows("w", w3, (G, K, N), _BF16, _on_current_device(w3))
+    _, sfb = B.moe_mxfp8_weight_bytes(G, K, N)
+    q = torch.empty((G, N, K), dtype=torch.float8_e4m3fn, device=w.device)
+    sf = torch.empty(sfb, dtype=torch.float8_e8m0fnu, device=w.device)
+    B.check(B.moe_mxfp8_quantize_weight(w3, G, K, N, q, sf, stream), "moe_mxfp8_quantize_weight")
+    return Mxfp8Linear(q, sf, G, K, N)
+
+
+def quantize_mxfp8_rows(x: torch.Tensor, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """x [T, D] bf16 -> (q [T, D] e4m3, scale [T, D/32] e8m0)."""
+    T, D = x.shape
+    dev = _on_current_device(x)
+    _rows("x", x, (T, D), _BF16, dev)
+    q = torch.empty((T, D), dtype=torch.float8_e4m3fn, device=dev)
+    scale = torch.empty((T, D // B.MXFP8_GROUP), dtype=torch.float8_e8m0fnu, device=dev)
+    B.check(B.moe_mxfp8_quantize_act(x, T, D, q, scale, stream), "moe_mxfp8_quantize_act")
+    return q, scale
+
+
+@dataclasses.dataclass
+class Mxfp8Weights:
+    dims: Dims
+    w_router: torch.Tensor
+    wg: Mxfp8Linear
+    wu: Mxfp8Linear
+    wd: Mxfp8Linear
+    sg: Mxfp8Linear
+    su: Mxfp8Linear
+    sd: Mxfp8Linear
+
+
+def quantize_mxfp8(dw: DeviceWeights, stream=None) -> Mxfp8Weights:
+    return Mxfp8Weights(dw.dims, dw.w_router,
+                        *(quantize_mxfp8_linear(t, stream) for t in (dw.wg, dw.wu, dw.wd, dw.sg, dw.su, dw.sd)))
+
+
+def mxfp8_params(mw: Mxfp8Weights, T: int, x=None, out=None, *, xq=None, xs=None, top_k=B.TOP_K, router_bias=None,
+                 res=None, workspace=None) -> B.MoeMxfp8Params:
+    d = mw.dims
+    res = res or BlockResult(out=out)
+    return B.MoeMxfp8Params(
+        T, top_k, d.embed_dim, d.num_experts, d.expert_dim, d.hidden_dim, B.ptr(x), B.ptr(xq), B.ptr(xs),
+        B.ptr(mw.w_router), B.ptr(router_bias), mw.wg.struct(), mw.wu.struct(), mw.wd.struct(), mw.sg.struct(),
+        mw.su.struct(), mw.sd.struct(), B.ptr(out), B.ptr(res.out_f32), B.ptr(res.idx), B.ptr(res.w), B.ptr(res.cnt),
+        B.ptr(workspace), 0 if workspace is None else workspace.numel())
+
+
+def mxfp8_workspace(mw: Mxfp8Weights, T: int, top_k: int = B.TOP_K) -> torch.Tensor:
+    """A workspace (uint8) for forward_mxfp8 calls of T tokens."""
+    need = B.moe_mxfp8_workspace_bytes(mxfp8_params(mw, T, top_k=top_k))
+    return torch.empty(need, dtype=torch.uint8, device=mw.w_router.device)
+
+
+def forward_mxfp8(
+    mw: Mxfp8Weights,
+    x: torch.Tensor,
+    *,
+    xq: torch.Tensor | None = None,
+    xs: torch.Tensor | None = None,
+    top_k: int = B.TOP_K,
+    router_bias: torch.Tensor | None = None,
+    debug: bool = False,
+    workspace: torch.Tensor | None = None,
+    out: torch.Tensor | None = None,
+    stream=None,
+) -> BlockResult:
+    """One block with MXFP8 weights and activations. x [T, D] bf16 feeds the
+    router; xq / xs are the same rows in MXFP8 (as add_rms_norm writes them),
+    without them the call quantises x."""
+    dev = _on_current_device(x)
+    T, D = x.shape[0], mw.dims.embed_dim
+    _rows("x", x, (T, D), _BF16, dev)
+    if xq is not None:
+        _rows("xq", xq, (T, D), _E4M3, dev)
+    if xs is not None:
+        _rows("xs", xs, (T, D // B.MXFP8_GROUP), _E8M0, dev)
+    if router_bias is not None:
+        _rows("router_bias", router_bias, (mw.dims.num_experts,), (torch.float32,), dev)
+    if workspace is not None:
+        _rows("workspace", workspace, workspace.shape, (torch.uint8,), dev)
+    out = torch.empty_like(x) if out is None else _rows("out", out, (T, D), _BF16, dev)
+    res = _result(out, mw.dims, top_k, debug)
+    p = mxfp8_params(mw, T, x, out, xq=xq, xs=xs, top_k=top_k, router_bias=router_bias, res=res, workspace=workspace)
+    B.check(B.moe_block_forward_mxfp8(p, stream), "moe_block_forward_mxfp8")
+    return res
+
+
+def _result(out: torch.Tensor, dims: Dims, top_k: int, debug: bool) -> BlockResult:
+    res = BlockResult(out=out)
+    if debug:
+        T, dev = out.shape[0], out.device
+        res.out_f32 = torch.empty((T, dims.embed_dim), dtype=torch.float32, device=dev)
+        res.idx = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        res.w = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+        res.cnt = torch.empty((dims.num_experts,), dtype=torch.int32, device=dev)
+    return res
+
+
 # ---------------------------------------------------------------- dense FFN
 
 

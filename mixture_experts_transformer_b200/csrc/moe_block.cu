@@ -18,6 +18,7 @@
 #include "norm.cuh"
 #include "permute.cuh"
 #include "router.cuh"
+#include "mxfp8.cuh"
 #include "nvfp4.cuh"
 #include "wq_gemm.cuh"
 
@@ -212,6 +213,11 @@ moe_status device_state(DeviceState** out) {
       if (cudaFuncSetAttribute(fp4_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kF4SmemBytes) !=
           cudaSuccess)
         return MOE_ERR_CUDA;
+      if (cudaFuncSetAttribute(mx_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmemBytes) !=
+              cudaSuccess ||
+          cudaFuncSetAttribute(mx_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmemBytes) !=
+              cudaSuccess)
+        return MOE_ERR_CUDA;
     }
     s.init = true;
   }
@@ -329,6 +335,10 @@ enum KernelId : int {
   kKAmax,
   kKPreNorm,
   kKGuard,
+  kKAddNorm,
+  kKScatterMx,
+  kKMxGateUp,
+  kKMxDown,
   kKCount
 };
 const char* const kKernelNames[kKCount] = {"router_logits", "router_topk", "build_masks", "route_scan",
@@ -337,7 +347,8 @@ const char* const kKernelNames[kKCount] = {"router_logits", "router_topk", "buil
                                            "nvfp4_weight_amax", "nvfp4_tensor_scale", "nvfp4_weight_quant",
                                            "nvfp4_act_quant", "route_scatter_fp4", "fp4_gemm_gateup",
                                            "fp4_gemm_down", "combine_norm", "amax", "rms_norm_pre",
-                                           "workspace_guard"};
+                                           "workspace_guard", "add_rms_norm", "route_scatter_mx", "mx_gemm_gateup",
+                                           "mx_gemm_down"};
 
 struct ProfRecord {
   int id;
@@ -653,11 +664,11 @@ moe_status enqueue_block(const moe_params* p, const Dims& d, const Layout& L, ui
 
 // ------------------------------------------------------------- NVFP4 host
 
-// [rows, cols] bytes; box 128 bytes x 128 rows; 128-byte swizzle.
-bool map_2d_u8(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols) {
+// [rows, cols] bytes; box 128 bytes x box_rows; 128-byte swizzle.
+bool map_2d_u8(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows = 128) {
   const cuuint64_t dims[2] = {cols, rows};
   const cuuint64_t strides[1] = {cols};
-  const cuuint32_t box[2] = {128, 128};
+  const cuuint32_t box[2] = {128, box_rows};
   const cuuint32_t estr[2] = {1, 1};
   return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -866,6 +877,210 @@ moe_status enqueue_block_fp4(const moe_nvfp4_params* p, const Dims& d, const Fp4
   if (p->cnt_out && cudaMemcpyAsync(p->cnt_out, cnt, d.E * 4, cudaMemcpyDeviceToDevice, st) != cudaSuccess)
     return MOE_ERR_CUDA;
   return MOE_OK;
+}
+
+// ------------------------------------------------------------- MXFP8 host
+
+size_t mx_q_bytes(size_t groups, size_t K, size_t N) { return groups * N * K; }
+size_t mx_sf_bytes(size_t groups, size_t K, size_t N) { return groups * ((N + 127) / 128) * ((K + 127) / 128) * 512; }
+
+// Whether [a, a + an) and [b, b + bn) share a byte.
+inline bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + bn && y < x + an;
+}
+
+// The caller's workspace, or the library's cached allocation. The latter grows
+// by freeing its predecessor, which a captured graph would still address: a
+// call that is being captured needs a workspace of its own.
+moe_status call_workspace(void* workspace, size_t given, size_t need, DeviceState* s, cudaStream_t st, uint8_t** ws) {
+  if (workspace) {
+    if ((reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0) return MOE_ERR_ALIGNMENT;
+    if (given < need) return MOE_ERR_WORKSPACE;
+    *ws = static_cast<uint8_t*>(workspace);
+    return MOE_OK;
+  }
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) return MOE_ERR_CUDA;
+  if (cap != cudaStreamCaptureStatusNone) return MOE_ERR_WORKSPACE;
+  void* w = nullptr;
+  MOE_TRY(library_workspace(s, need, &w));
+  *ws = static_cast<uint8_t*>(w);
+  return MOE_OK;
+}
+
+// The MXFP8 workspace: the routing part and the quantised activations in a
+// 128-padded expert-major row space, as the NVFP4 layout.
+struct MxLayout {
+  Layout r;
+  size_t xq_perm, xsf_perm, xq_tok, xsf_tok, hq, hsf, hsq, hssf, y, s;
+  size_t total;
+  long long r_pad, t_pad;
+};
+
+MxLayout make_mx_layout(const Dims& d) {
+  MxLayout M{};
+  const Fp4Layout F = make_fp4_layout(d);
+  M.r = F.r;
+  M.r_pad = F.r_pad;
+  M.t_pad = F.t_pad;
+  const size_t T = d.T, rp = F.r_pad, tp = F.t_pad;
+  size_t o = F.xq_perm;  // the routing part ends here
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align_up(o + bytes, kAlign);
+    return at;
+  };
+  M.xq_perm = take(rp * d.D);
+  M.xsf_perm = take(mx_sf_bytes(1, d.D, rp));
+  M.xq_tok = take(tp * d.D);
+  M.xsf_tok = take(mx_sf_bytes(1, d.D, tp));
+  M.hq = take(rp * d.F);
+  M.hsf = take(mx_sf_bytes(1, d.F, rp));
+  M.hsq = take(tp * d.S);
+  M.hssf = take(mx_sf_bytes(1, d.S, tp));
+  M.y = take(rp * d.D * 2);
+  M.s = take(T * d.D * 4);
+  M.total = o;
+  M.r.total = o;
+  return M;
+}
+
+Dims mx_dims_of(const moe_mxfp8_params* p) {
+  Dims d;
+  d.T = p->T;
+  d.k = p->top_k_experts;
+  d.D = p->embed_dim ? p->embed_dim : MOE_EMBED_DIM;
+  d.E = p->num_experts ? p->num_experts : MOE_NUM_EXPERTS;
+  d.F = p->expert_dim ? p->expert_dim : MOE_EXPERT_DIM;
+  d.S = p->hidden_dim ? p->hidden_dim : MOE_HIDDEN_DIM;
+  d.e0 = 0;
+  d.el = d.E;
+  return d;
+}
+
+moe_status check_mx_args(const moe_mxfp8_params* p, Dims* d) {
+  if (!p) return MOE_ERR_INVALID_ARG;
+  *d = mx_dims_of(p);
+  if (!dims_ok(*d)) return MOE_ERR_INVALID_ARG;
+  if (d->T == 0) return MOE_OK;
+  const void* req[] = {p->x,    p->w_router, p->wg.q,  p->wu.q,  p->wd.q,  p->sg.q,  p->su.q,
+                       p->sd.q, p->wg.sf,    p->wu.sf, p->wd.sf, p->sg.sf, p->su.sf, p->sd.sf};
+  for (const void* q : req)
+    if (!q) return MOE_ERR_INVALID_ARG;
+  for (const void* q : req)
+    if (!aligned16(q)) return MOE_ERR_ALIGNMENT;
+  if (!p->out && !p->out_f32) return MOE_ERR_INVALID_ARG;
+  if (!p->xq != !p->xs) return MOE_ERR_INVALID_ARG;  // the quantised rows come with their scales
+  const void* opt16[] = {p->out, p->out_f32, p->xq, p->xs};
+  for (const void* q : opt16)
+    if (q && !aligned16(q)) return MOE_ERR_ALIGNMENT;
+  const void* opt4[] = {p->router_bias, p->idx_out, p->w_out, p->cnt_out};
+  for (const void* q : opt4)
+    if (q && !aligned4(q)) return MOE_ERR_ALIGNMENT;
+  const size_t n = static_cast<size_t>(d->T) * d->D;
+  const struct {
+    const void* at;
+    size_t bytes;
+  } ins[] = {{p->x, n * 2}, {p->xq, n}, {p->xs, n / kMxGroup}};
+  for (const auto& i : ins)
+    if (overlap(i.at, i.bytes, p->out, n * 2) || overlap(i.at, i.bytes, p->out_f32, n * 4)) return MOE_ERR_INVALID_ARG;
+  if (overlap(p->out, n * 2, p->out_f32, n * 4)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+moe_status enqueue_block_mx(const moe_mxfp8_params* p, const Dims& d, const MxLayout& M, uint8_t* ws, DeviceState* s,
+                            cudaStream_t st) {
+  const Layout& L = M.r;
+  int32_t* idx = reinterpret_cast<int32_t*>(ws + L.idx);
+  float* w = reinterpret_cast<float*>(ws + L.w);
+  int32_t* cnt = reinterpret_cast<int32_t*>(ws + L.cnt);
+  int32_t* off = reinterpret_cast<int32_t*>(ws + L.off);
+  int32_t* row_of = reinterpret_cast<int32_t*>(ws + L.row_of);
+  const uint32_t* masks = reinterpret_cast<const uint32_t*>(ws + L.masks);
+  int32_t* base = reinterpret_cast<int32_t*>(ws + L.base);
+  TileCounts* counts = reinterpret_cast<TileCounts*>(ws + L.counts);
+  const int rp = static_cast<int>(M.r_pad), tp = static_cast<int>(M.t_pad);
+
+  MOE_TRY(enqueue_route(d, L, ws, p->x, p->w_router, p->router_bias, idx, w, st));
+  {
+    LaunchScope ls_(kKRouteScan, st);
+    MOE_TRY(ls_.done(launch_k(route_scan_kernel, kScanCtas, kScanThreads, 0, st, masks, L.nchunks, d.T, d.E, d.F, d.S,
+                              d.D, base, cnt, off, reinterpret_cast<Tile*>(ws + L.tiles_gu),
+                              reinterpret_cast<Tile*>(ws + L.tiles_dn), counts, 1, 256, 128, 0, 0, 0, d.E)));
+  }
+  {
+    const int blocks = static_cast<int>(std::min<long long>((d.T + 7LL) / 8, 148LL * 64));  // a warp per token
+    LaunchScope ls_(kKScatterMx, st);
+    MOE_TRY(ls_.done(launch_k(route_scatter_mx_kernel, blocks, 256, 0, st, idx, masks, base, d.T, d.k, d.E, d.D,
+                              static_cast<const __nv_bfloat16*>(p->x), static_cast<const uint8_t*>(p->xq),
+                              static_cast<const uint8_t*>(p->xs), row_of, ws + M.xq_perm, ws + M.xsf_perm,
+                              ws + M.xq_tok, ws + M.xsf_tok, rp, s->err)));
+  }
+  // the shared MLP reads the caller's quantised rows in place
+  const void* xtok = p->xq ? static_cast<const void*>(p->xq) : ws + M.xq_tok;
+
+  MxParams gu;
+  std::memset(&gu, 0, sizeof(gu));
+  if (!map_2d_u8(&gu.tmA[0], ws + M.xq_perm, rp, d.D) || !map_2d_u8(&gu.tmAs[0], ws + M.xq_perm, rp, d.D, kMxASmallRows) ||
+      !map_3d_u8(&gu.tmB0[0], p->wg.q, d.E, d.F, d.D) || !map_3d_u8(&gu.tmB1[0], p->wu.q, d.E, d.F, d.D) ||
+      !map_2d_u8(&gu.tmA[1], xtok, d.T, d.D) || !map_2d_u8(&gu.tmAs[1], xtok, d.T, d.D, kMxASmallRows) ||
+      !map_3d_u8(&gu.tmB0[1], p->sg.q, 1, d.S, d.D) || !map_3d_u8(&gu.tmB1[1], p->su.q, 1, d.S, d.D))
+    return MOE_ERR_CUDA;
+  gu.prob[0] = MxProblem{d.D, d.F, d.E, rp, ws + M.xsf_perm, p->wg.sf, p->wu.sf, ws + M.hq, ws + M.hsf, d.F, 0};
+  gu.prob[1] = MxProblem{d.D, d.S, 1, tp, ws + M.xsf_tok, p->sg.sf, p->su.sf, ws + M.hsq, ws + M.hssf, d.S, 0};
+  gu.nprob = 2;
+  gu.tiles = reinterpret_cast<const Tile*>(ws + L.tiles_gu);
+  gu.num_tiles = &counts->gateup;
+  gu.next_tile = &counts->next_gateup;
+  gu.err = s->err;
+  {
+    LaunchScope ls_(kKMxGateUp, st);
+    MOE_TRY(ls_.done(
+        launch_k(mx_gemm_kernel<true>, std::min(s->sm_count, L.max_tiles_gu), kMxThreads, kMxSmemBytes, st, gu)));
+  }
+
+  MxParams dn;
+  std::memset(&dn, 0, sizeof(dn));
+  if (!map_2d_u8(&dn.tmA[0], ws + M.hq, rp, d.F) || !map_2d_u8(&dn.tmAs[0], ws + M.hq, rp, d.F, kMxASmallRows) ||
+      !map_2d_u8(&dn.tmA[1], ws + M.hsq, tp, d.S) || !map_2d_u8(&dn.tmAs[1], ws + M.hsq, tp, d.S, kMxASmallRows) ||
+      !map_3d_u8(&dn.tmB0[0], p->wd.q, d.E, d.D, d.F) || !map_3d_u8(&dn.tmB0[1], p->sd.q, 1, d.D, d.S) ||
+      !map_3d_u8(&dn.tmBw[0], p->wd.q, d.E, d.D, d.F, 256) || !map_3d_u8(&dn.tmBw[1], p->sd.q, 1, d.D, d.S, 256))
+    return MOE_ERR_CUDA;
+  float* sbuf = reinterpret_cast<float*>(ws + M.s);
+  dn.prob[0] = MxProblem{d.F, d.D, d.E, rp, ws + M.hsf, p->wd.sf, p->wd.sf, ws + M.y, nullptr, d.D, 0};
+  dn.prob[1] = MxProblem{d.S, d.D, 1, tp, ws + M.hssf, p->sd.sf, p->sd.sf, sbuf, nullptr, d.D, 1};
+  dn.nprob = 2;
+  dn.tiles = reinterpret_cast<const Tile*>(ws + L.tiles_dn);
+  dn.num_tiles = &counts->down;
+  dn.next_tile = &counts->next_down;
+  dn.err = s->err;
+  {
+    LaunchScope ls_(kKMxDown, st);
+    MOE_TRY(ls_.done(
+        launch_k(mx_gemm_kernel<false>, std::min(s->sm_count, L.max_tiles_dn), kMxThreads, kMxSmemBytes, st, dn)));
+  }
+  {
+    LaunchScope ls_(kKCombine, st);
+    const int dsplit = std::max(1, std::min(4, (2 * s->sm_count) / std::max(1, d.T)));
+    MOE_TRY(ls_.done(launch_k(combine_kernel, dim3(d.T, dsplit), 128, 0, st, sbuf,
+                              reinterpret_cast<const __nv_bfloat16*>(ws + M.y), row_of, w, d.T, d.k, d.D, rp,
+                              static_cast<__nv_bfloat16*>(p->out), p->out_f32, s->err)));
+  }
+  const size_t R = static_cast<size_t>(d.T) * d.k;
+  if (p->idx_out && cudaMemcpyAsync(p->idx_out, idx, R * 4, cudaMemcpyDeviceToDevice, st) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  if (p->w_out && cudaMemcpyAsync(p->w_out, w, R * 4, cudaMemcpyDeviceToDevice, st) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  if (p->cnt_out && cudaMemcpyAsync(p->cnt_out, cnt, d.E * 4, cudaMemcpyDeviceToDevice, st) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return MOE_OK;
+}
+
+template <int TPR, int NV>
+cudaError_t launch_add_norm(const AddNormParams& P, cudaStream_t st) {
+  constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
+  return launch_k(add_rms_norm_kernel<TPR, NV>, (P.T + kRows - 1) / kRows, TPR < 128 ? 128 : TPR, 0, st, P);
 }
 
 // -------------------------------------------------- weight-only formats
@@ -1680,6 +1895,131 @@ moe_status moe_nvfp4_calibrate(const moe_params* p, float* amax, float* scales, 
   // the three tensor scales G = 448 * 6 / amax (1 for an all-zero tensor)
   LaunchScope ls_(kKTensorScale, st);
   return ls_.done(launch_k(tensor_scale_kernel, 1, 32, 0, st, reinterpret_cast<const uint32_t*>(amax), scales, 3));
+}
+
+moe_status moe_add_rms_norm(const moe_norm_params* p, void* stream) {
+  ApiRange nvtx_range_("moe_add_rms_norm");
+  t_launches = 0;
+  if (!p) return MOE_ERR_INVALID_ARG;
+  const int D = p->embed_dim ? p->embed_dim : MOE_EMBED_DIM;
+  const float eps = p->eps == 0.f ? 1e-6f : p->eps;
+  if (p->T < 0 || D <= 0 || D % 8 || D > 16384 || !(eps > 0.f) || eps > 1e30f) return MOE_ERR_INVALID_ARG;
+  if (p->T == 0) return MOE_OK;
+  if (!p->x || !p->q != !p->scale || (p->q && D % kMxGroup)) return MOE_ERR_INVALID_ARG;
+  if (!p->sum && !p->y && !p->q) return MOE_ERR_INVALID_ARG;  // an output is needed
+  const void* all[] = {p->x, p->residual, p->gamma_post, p->gamma, p->sum, p->y, p->q};
+  for (const void* a : all)
+    if (a && !aligned16(a)) return MOE_ERR_ALIGNMENT;
+  const size_t n = static_cast<size_t>(p->T) * D;
+  const struct {
+    const void* at;
+    size_t bytes;
+  } outs[] = {{p->sum, n * 2}, {p->y, n * 2}, {p->q, n}, {p->scale, n / kMxGroup}},
+    ins[] = {{p->x, n * 2}, {p->residual, n * 2}},
+    gammas[] = {{p->gamma_post, static_cast<size_t>(D) * 2}, {p->gamma, static_cast<size_t>(D) * 2}};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i].at, outs[i].bytes, outs[j].at, outs[j].bytes)) return MOE_ERR_INVALID_ARG;
+    // a bf16 output may replace x or residual, row for row; no other overlap
+    for (const auto& in : ins)
+      if (overlap(outs[i].at, outs[i].bytes, in.at, in.bytes) && !(i < 2 && outs[i].at == in.at))
+        return MOE_ERR_INVALID_ARG;
+    for (const auto& g : gammas)
+      if (overlap(outs[i].at, outs[i].bytes, g.at, g.bytes)) return MOE_ERR_INVALID_ARG;
+  }
+  DeviceState* s = nullptr;
+  MOE_TRY(device_state(&s));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const AddNormParams P{p->T,
+                        D,
+                        eps,
+                        static_cast<const __nv_bfloat16*>(p->x),
+                        static_cast<const __nv_bfloat16*>(p->residual),
+                        static_cast<const __nv_bfloat16*>(p->gamma_post),
+                        static_cast<const __nv_bfloat16*>(p->gamma),
+                        static_cast<__nv_bfloat16*>(p->sum),
+                        static_cast<__nv_bfloat16*>(p->y),
+                        static_cast<uint8_t*>(p->q),
+                        static_cast<uint8_t*>(p->scale)};
+  LaunchScope ls_(kKAddNorm, st);
+  const int nvec = D / 8;  // 16-byte vectors of a row
+  return ls_.done(nvec <= 32        ? launch_add_norm<32, 1>(P, st)
+                  : nvec <= 4 * 32  ? launch_add_norm<32, 4>(P, st)
+                  : nvec <= 3 * 128 ? launch_add_norm<128, 3>(P, st)
+                  : nvec <= 4 * 128 ? launch_add_norm<128, 4>(P, st)
+                  : nvec <= 2 * 512 ? launch_add_norm<512, 2>(P, st)
+                                    : launch_add_norm<512, 4>(P, st));
+}
+
+moe_status moe_mxfp8_weight_bytes(int groups, int K, int N, size_t* q_bytes, size_t* sf_bytes) {
+  if (groups <= 0 || K <= 0 || N <= 0 || K % 64 || N % 64) return MOE_ERR_INVALID_ARG;
+  if (q_bytes) *q_bytes = mx_q_bytes(groups, K, N);
+  if (sf_bytes) *sf_bytes = mx_sf_bytes(groups, K, N);
+  return MOE_OK;
+}
+
+moe_status moe_mxfp8_quantize_weight(const void* w, int groups, int K, int N, uint8_t* q, uint8_t* sf, void* stream) {
+  ApiRange nvtx_range_("moe_mxfp8_quantize_weight");
+  t_launches = 0;
+  if (groups <= 0 || K <= 0 || N <= 0 || K % 64 || N % 64 || groups > 65535) return MOE_ERR_INVALID_ARG;
+  if (!w || !q || !sf) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(w) || !aligned16(q) || !aligned16(sf)) return MOE_ERR_ALIGNMENT;
+  const long long items = static_cast<long long>(N) * (K / kMxGroup);
+  if ((items + 255) / 256 > 0x7FFFFFFFLL) return MOE_ERR_INVALID_ARG;
+  const size_t wb = mx_q_bytes(groups, K, N) * 2;
+  if (overlap(w, wb, q, wb / 2) || overlap(w, wb, sf, mx_sf_bytes(groups, K, N)) ||
+      overlap(q, wb / 2, sf, mx_sf_bytes(groups, K, N)))
+    return MOE_ERR_INVALID_ARG;
+  DeviceState* s = nullptr;
+  MOE_TRY(device_state(&s));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (cudaMemsetAsync(sf, 0, mx_sf_bytes(groups, K, N), st) != cudaSuccess) return MOE_ERR_CUDA;
+  LaunchScope ls_(kKWeightQuant, st);
+  return ls_.done(launch_k(mx_weight_quant_kernel, dim3(static_cast<unsigned>((items + 255) / 256), groups), 256, 0, st,
+                           static_cast<const __nv_bfloat16*>(w), K, N, q, sf));
+}
+
+moe_status moe_mxfp8_quantize_act(const void* x, int rows, int K, uint8_t* q, uint8_t* scale, void* stream) {
+  ApiRange nvtx_range_("moe_mxfp8_quantize_act");
+  t_launches = 0;
+  if (rows < 0 || K <= 0 || K % kMxGroup) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!x || !q || !scale) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(q)) return MOE_ERR_ALIGNMENT;
+  const size_t n = static_cast<size_t>(rows) * K;
+  if (overlap(x, n * 2, q, n) || overlap(x, n * 2, scale, n / kMxGroup) || overlap(q, n, scale, n / kMxGroup))
+    return MOE_ERR_INVALID_ARG;
+  DeviceState* s = nullptr;
+  MOE_TRY(device_state(&s));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const size_t groups = n / kMxGroup;
+  const int blocks = static_cast<int>(std::min<size_t>((groups + 255) / 256, static_cast<size_t>(s->sm_count) * 32));
+  LaunchScope ls_(kKActQuant, st);
+  return ls_.done(
+      launch_k(mx_act_quant_kernel, blocks, 256, 0, st, static_cast<const __nv_bfloat16*>(x), groups, q, scale));
+}
+
+size_t moe_mxfp8_workspace_bytes(const moe_mxfp8_params* p) {
+  if (!p) return 0;
+  const Dims d = mx_dims_of(p);
+  if (!dims_ok(d)) return 0;
+  return make_mx_layout(d).total;
+}
+
+moe_status moe_block_forward_mxfp8(const moe_mxfp8_params* p, void* stream) {
+  ApiRange nvtx_range_("moe_block_forward_mxfp8");
+  t_launches = 0;
+  Dims d;
+  MOE_TRY(check_mx_args(p, &d));
+  if (d.T == 0) return MOE_OK;
+  DeviceState* s = nullptr;
+  MOE_TRY(device_state(&s));
+  if (!encode_fn()) return MOE_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const MxLayout M = make_mx_layout(d);
+  uint8_t* ws = nullptr;
+  MOE_TRY(call_workspace(p->workspace, p->workspace_bytes, M.total, s, st, &ws));
+  return enqueue_block_mx(p, d, M, ws, s, st);
 }
 
 size_t moe_dense_workspace_bytes(const moe_dense_params* p) {

@@ -1,0 +1,573 @@
+// MXFP8 variant of the block: expert and shared Linears with e4m3 weights and
+// e4m3 activations, both in groups of 32 along the reduction with one
+// power-of-two scale per group (mxformat.cuh); the router stays bf16.
+//
+// Storage (also the tcgen05 block-scaled operand layout):
+//   codes  [rows][K] bytes, K-major;
+//   scales [ceil(rows/128)][ceil(K/128)][512] bytes (mx_sf_offset), rows and
+//          groups past the end hold code 0.
+//
+// The GEMM (mx_gemm_kernel) has the NVFP4 GEMM's structure with
+// `tcgen05.mma.kind::mxf8f6f4.block_scale.block32`: one 128-K stage is 128
+// bytes of every operand row and exactly one scale atom per 128-row block, so
+// a stage's scales are one 512-byte copy each and go to one TMEM slot; the four
+// 32-K MMAs of the stage pick their byte of the slot's words by the scale id of
+// the instruction descriptor. A reduction that ends inside a stage (K a multiple
+// of 64) issues only the MMAs it has.
+#pragma once
+
+#include "grouped_gemm.cuh"
+#include "mxformat.cuh"
+#include "nvfp4.cuh"
+#include "ptx.cuh"
+#include "router.cuh"
+
+namespace moe {
+
+__host__ __device__ constexpr int mx_kblocks(int K) { return (K + 127) / 128; }
+
+// ------------------------------------------------------------- quantisers
+
+__device__ __forceinline__ void load32_bf16(const __nv_bfloat16* p, float (&v)[32]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p) + q);
+    const __nv_bfloat16* pa = reinterpret_cast<const __nv_bfloat16*>(&a);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[8 * q + i] = __bfloat162float(pa[i]);
+  }
+}
+
+// One thread per (n, 32-group of K) of w [G][K][N] (N contiguous): codes into
+// q [G][N][K], scale into the atoms of sf (cleared beforehand).
+__global__ void mx_weight_quant_kernel(const __nv_bfloat16* __restrict__ w, int K, int N, uint8_t* __restrict__ q,
+                                       uint8_t* __restrict__ sf) {
+  pdl_wait_then_release();
+  const size_t g = blockIdx.y;
+  const int groups = K / kMxGroup;
+  const long long idx = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (idx >= static_cast<long long>(N) * groups) return;
+  const int n = static_cast<int>(idx % N);
+  const int kg = static_cast<int>(idx / N);
+  const __nv_bfloat16* src = w + (g * K + kg * kMxGroup) * N + n;
+  float v[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __bfloat162float(src[static_cast<size_t>(i) * N]);
+  uint4 codes[2];
+  const uint32_t sc = mx_group(v, codes);
+  uint4* dst = reinterpret_cast<uint4*>(q + (g * N + n) * K + kg * kMxGroup);
+  dst[0] = codes[0];
+  dst[1] = codes[1];
+  const size_t nb = (N + 127) / 128;
+  sf[g * nb * mx_kblocks(K) * 512 + mx_sf_offset(n, kg, mx_kblocks(K))] = static_cast<uint8_t>(sc);
+}
+
+// x [rows][K] bf16 -> q [rows][K], scale [rows][K/32]; one thread per group.
+__global__ void mx_act_quant_kernel(const __nv_bfloat16* __restrict__ x, size_t groups, uint8_t* __restrict__ q,
+                                    uint8_t* __restrict__ scale) {
+  pdl_wait_then_release();
+  for (size_t i = blockIdx.x * static_cast<size_t>(blockDim.x) + threadIdx.x; i < groups;
+       i += static_cast<size_t>(gridDim.x) * blockDim.x) {
+    float v[32];
+    load32_bf16(x + i * kMxGroup, v);
+    uint4 codes[2];
+    scale[i] = static_cast<uint8_t>(mx_group(v, codes));
+    reinterpret_cast<uint4*>(q)[2 * i] = codes[0];
+    reinterpret_cast<uint4*>(q)[2 * i + 1] = codes[1];
+  }
+}
+
+// The MXFP8 block's scatter: one warp per token, as route_scatter_fp4_kernel.
+// The row's codes come from x (quantised here, once) or, already in MXFP8,
+// from xq / xs (codes [T][D], scales [T][D/32]); each lane handles whole
+// groups. Written: the codes and scale atoms of the token's k routed rows, the
+// token-order scale atoms (the shared MLP's), and - without xq, which the shared
+// MLP reads in place - the token-order codes.
+__global__ void __launch_bounds__(256) route_scatter_mx_kernel(
+    const int32_t* __restrict__ idx, const uint32_t* __restrict__ masks, const int32_t* __restrict__ base, int T,
+    int k, int E, int D, const __nv_bfloat16* __restrict__ x, const uint8_t* __restrict__ xq,
+    const uint8_t* __restrict__ xs, int32_t* __restrict__ row_of, uint8_t* __restrict__ xq_perm,
+    uint8_t* __restrict__ xsf_perm, uint8_t* __restrict__ xq_tok, uint8_t* __restrict__ xsf_tok, int rows,
+    uint32_t* __restrict__ err) {
+  __shared__ int s_rows[8][128];  // k <= num_experts <= 128
+  pdl_wait_then_release();
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int ng = D / kMxGroup, kb = mx_kblocks(D);
+  for (int t = blockIdx.x * 8 + wid; t < T; t += gridDim.x * 8) {
+    for (int j = lane; j < k; j += 32) {
+      const size_t a = static_cast<size_t>(t) * k + j;
+      const int e = __ldg(idx + a);
+      int row = -1;
+      if (e >= 0 && e < E) {
+        const size_t cw = static_cast<size_t>(t / kMaskTokens) * E + e;
+        const uint32_t below = __ldg(masks + cw) & ((1u << (t & (kMaskTokens - 1))) - 1u);
+        row = __ldg(base + cw) + __popc(below);
+        if (row < 0 || row >= rows) {  // never write outside the routed-row buffers
+          atomicOr(err, kErrBadIndex);
+          row = -1;
+        } else {
+          row_of[a] = row;
+        }
+      }
+      s_rows[wid][j] = row;
+    }
+    __syncwarp();
+    for (int g0 = 0; g0 < ng; g0 += 32) {
+      const int g = g0 + lane;
+      const bool in = g < ng;
+      uint4 codes[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+      uint32_t sc = 0;
+      if (in) {
+        if (xq) {
+          const uint4* src = reinterpret_cast<const uint4*>(xq + static_cast<size_t>(t) * D) + 2 * g;
+          codes[0] = __ldg(src);
+          codes[1] = __ldg(src + 1);
+          sc = __ldg(xs + static_cast<size_t>(t) * ng + g);
+        } else {
+          float v[32];
+          load32_bf16(x + static_cast<size_t>(t) * D + g * kMxGroup, v);
+          sc = mx_group(v, codes);
+        }
+      }
+      // the four scales of a 128-K block are one aligned word of the atom
+      uint32_t scw = sc << (8 * (lane & 3));
+      scw |= __shfl_xor_sync(0xffffffffu, scw, 1);
+      scw |= __shfl_xor_sync(0xffffffffu, scw, 2);
+      if (!in) continue;
+      const bool word = (lane & 3) == 0;
+      if (!xq) {
+        uint4* qt = reinterpret_cast<uint4*>(xq_tok + static_cast<size_t>(t) * D) + 2 * g;
+        qt[0] = codes[0];
+        qt[1] = codes[1];
+      }
+      if (word) *reinterpret_cast<uint32_t*>(xsf_tok + mx_sf_offset(t, g, kb)) = scw;
+      for (int j = 0; j < k; ++j) {
+        const int row = s_rows[wid][j];
+        if (row < 0) continue;
+        uint4* qp = reinterpret_cast<uint4*>(xq_perm + static_cast<size_t>(row) * D) + 2 * g;
+        qp[0] = codes[0];
+        qp[1] = codes[1];
+        if (word) *reinterpret_cast<uint32_t*>(xsf_perm + mx_sf_offset(row, g, kb)) = scw;
+      }
+    }
+    __syncwarp();
+  }
+}
+
+// ------------------------------------------------------------- MXFP8 GEMM
+
+constexpr int kMxKStage = 128;                    // K elements (= bytes of a row) per stage
+constexpr int kMxABytes = 128 * kMxKStage;        // 128 rows
+constexpr int kMxBBytes = 2 * 128 * kMxKStage;    // two 128-row blocks
+constexpr int kMxSfBytes = 512;                   // one atom per 128-row block
+constexpr int kMxStages = 4;
+constexpr int kMxThreads = 320 + 128;             // producer, MMA, 8 epilogue warps, 4 scale warps
+constexpr int kMxASmallRows = 32;                 // rows of the small A box
+constexpr int kMxSmemBytes =
+    kMxStages * (kMxABytes + kMxBBytes + 3 * kMxSfBytes) + 8 * kF4StgWarpBytes + 1024 + 512;
+
+struct MxProblem {
+  int K;          // multiple of 64
+  int N;          // multiple of 64
+  int groups;
+  int a_rows;     // rows the tiles may start in (a multiple of 128)
+  const uint8_t* sfa;   // [a_rows/128][ceil(K/128)][512]
+  const uint8_t* sfb0;  // [groups][ceil(N/128)][ceil(K/128)][512]
+  const uint8_t* sfb1;  // (up; GATEUP only)
+  void* out;            // GATEUP: codes [rows][N]; DOWN: bf16 / fp32 [rows][ldo]
+  uint8_t* out_sf;      // GATEUP: scales [rows/128][ceil(N/128)][512]
+  int ldo;
+  int out_f32;
+};
+
+struct MxParams {
+  CUtensorMap tmA[2];   // codes [rows][K] u8, box 128 x 128, 128-byte swizzle
+  CUtensorMap tmAs[2];  // the same, box 128 x 32: tiles of at most 32 rows copy only those
+  CUtensorMap tmB0[2];  // codes [groups][N][K] u8, box 128 x 128 x 1
+  CUtensorMap tmB1[2];
+  CUtensorMap tmBw[2];  // down: box 128 x 256 x 1
+  MxProblem prob[2];
+  int nprob;
+  const Tile* tiles;
+  const int32_t* num_tiles;
+  int32_t* next_tile;
+  uint32_t* err;
+};
+
+// Instruction descriptor of kind::mxf8f6f4 (e4m3 A and B, ue8m0 scales),
+// K-major A and B, M = 128; sf_id picks the scale byte of A's and B's words.
+__host__ __device__ constexpr uint32_t idesc_mxf8_m128(int n, int sf_id) {
+  return (static_cast<uint32_t>(sf_id) << 4)        // B scale id
+         | (static_cast<uint32_t>(n >> 3) << 17)    // N / 8
+         | (1u << 23)                               // scales are ue8m0
+         | (static_cast<uint32_t>(128 >> 4) << 24)    // M / 16
+         | (static_cast<uint32_t>(sf_id) << 29);    // A scale id
+}
+
+__device__ __forceinline__ void umma_mxf8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+      : "memory");
+}
+
+// TMEM columns [0, 256): the accumulator (GATEUP: gate 0..127, up 128..255;
+// DOWN: output columns n0 .. n0+255); from 256: one scale slot per stage, A
+// scales at +0, B block 0 at +4, B block 1 at +8.
+template <bool GATEUP>
+__global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_constant__ MxParams P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + kMxStages * kMxABytes;
+  uint8_t* sSf = sB + kMxStages * kMxBBytes;  // per stage: A atom, B block 0 atom, B block 1 atom
+  uint8_t* sStg = sSf + kMxStages * 3 * kMxSfBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sStg + 8 * kF4StgWarpBytes);
+  uint64_t* empty = full + kMxStages;
+  uint64_t* acc_full = empty + kMxStages;
+  uint64_t* acc_empty = acc_full + 1;
+  uint64_t* drain = acc_empty + 1;
+  uint64_t* sf_ready = drain + 1;  // a stage's scale atoms are in TMEM (one arrival per scale warp)
+  uint64_t* tile_full = sf_ready + kMxStages;
+  uint64_t* tile_empty = tile_full + kTileRing;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tile_empty + kTileRing);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* tile_ring = abort_flag + 1;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMxStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&sf_ready[s], 4);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, 8);  // one arrival per epilogue warp
+    mbar_init(drain, 1);
+    for (int r = 0; r < kTileRing; ++r) {
+      mbar_init(&tile_full[r], 1);
+      mbar_init(&tile_empty[r], 1 + 8 + 4);  // MMA thread, epilogue and scale warps read each index
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    for (int p = 0; p < P.nprob; ++p) {
+      tma_prefetch_desc(&P.tmA[p]);
+      tma_prefetch_desc(&P.tmAs[p]);
+      tma_prefetch_desc(&P.tmB0[p]);
+      tma_prefetch_desc(GATEUP ? &P.tmB1[p] : &P.tmBw[p]);
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait_then_release();
+  const int num_tiles = *P.num_tiles;
+  // Tile indices: the producer takes them from the work counter and publishes
+  // them in the ring (-1 ends the work), the other roles read them in order.
+  int rs = 0;
+  uint32_t rph = 0;
+  auto next_tile = [&](bool whole_warp) -> int {
+    int ti = -1;
+    if (lane == 0) {
+      if (mbar_wait(&tile_full[rs], rph, abort_flag, P.err)) {
+        ti = tile_ring[rs];
+        mbar_arrive(&tile_empty[rs]);
+      }
+    }
+    if (whole_warp) ti = __shfl_sync(0xffffffffu, ti, 0);
+    if (++rs == kTileRing) {
+      rs = 0;
+      rph ^= 1;
+    }
+    return ti;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------ TMA producer
+      int s = 0, issued = 0;
+      uint32_t ph = 0;
+      int ti = atomicAdd(P.next_tile, 1);
+      while (true) {
+        if (!mbar_wait(&tile_empty[rs], rph ^ 1, abort_flag, P.err)) break;
+        const Tile tile = ti < num_tiles ? P.tiles[ti] : Tile{};
+        const int p = tile.pg >> 16, g = tile.pg & 0xFFFF;
+        bool ok = true;
+        if (ti < num_tiles) {  // checked before the other roles see the tile
+          ok = p < P.nprob;
+          if (ok) {
+            const MxProblem& pr = P.prob[p];
+            ok = g < pr.groups && tile.row0 >= 0 && tile.row0 < pr.a_rows && !(tile.row0 & 127) && tile.n0 >= 0 &&
+                 tile.n0 < pr.N && !(tile.n0 & 127);
+          }
+          if (!ok) atomicOr(P.err, kErrBadTile);
+        }
+        tile_ring[rs] = ok && ti < num_tiles ? ti : -1;
+        mbar_arrive(&tile_full[rs]);
+        if (++rs == kTileRing) {
+          rs = 0;
+          rph ^= 1;
+        }
+        if (!ok || ti >= num_tiles) break;
+        const int next = atomicAdd(P.next_tile, 1);  // its latency hides behind this tile's loads
+        const MxProblem& pr = P.prob[p];
+        const int kb = mx_kblocks(pr.K);
+        const int nbr = (pr.N + 127) / 128;
+        const int nb0 = tile.n0 >> 7;
+        const int nb1 = GATEUP ? nb0 : nb0 + 1;
+        const uint8_t* sfa = pr.sfa + static_cast<size_t>(tile.row0 >> 7) * kb * 512;
+        const uint8_t* sfb0 = pr.sfb0 + (static_cast<size_t>(g) * nbr + nb0) * kb * 512;
+        const uint8_t* sfb1 = (GATEUP ? pr.sfb1 : pr.sfb0) + (static_cast<size_t>(g) * nbr + nb1) * kb * 512;
+        const bool two_b = GATEUP || (tile.n0 + 128 < pr.N);
+        const bool small = tile.rows <= kMxASmallRows;
+        const uint32_t bytes = (small ? kMxASmallRows * kMxKStage : kMxABytes) +
+                               (two_b ? 2 : 1) * (kMxBBytes / 2) + kMxSfBytes * (two_b ? 3 : 2);
+        for (int ks = 0; ks < kb; ++ks) {
+          if (!mbar_wait(&empty[s], ph ^ 1, abort_flag, P.err)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[s], bytes);
+          tma_load_2d(sA + s * kMxABytes, small ? &P.tmAs[p] : &P.tmA[p], &full[s], ks * kMxKStage, tile.row0);
+          if (!GATEUP && two_b) {
+            tma_load_3d(sB + s * kMxBBytes, &P.tmBw[p], &full[s], ks * kMxKStage, tile.n0, g);  // 256 rows
+          } else {
+            tma_load_3d(sB + s * kMxBBytes, &P.tmB0[p], &full[s], ks * kMxKStage, tile.n0, g);
+            if (two_b)
+              tma_load_3d(sB + s * kMxBBytes + kMxBBytes / 2, &P.tmB1[p], &full[s], ks * kMxKStage, tile.n0, g);
+          }
+          uint8_t* sf = sSf + s * 3 * kMxSfBytes;
+          bulk_load(sf, sfa + static_cast<size_t>(ks) * 512, kMxSfBytes, &full[s]);
+          bulk_load(sf + kMxSfBytes, sfb0 + static_cast<size_t>(ks) * 512, kMxSfBytes, &full[s]);
+          if (two_b) bulk_load(sf + 2 * kMxSfBytes, sfb1 + static_cast<size_t>(ks) * 512, kMxSfBytes, &full[s]);
+          ++issued;
+          if (++s == kMxStages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (!ok) break;
+        ti = next;
+      }
+      if (*abort_flag) {  // wait for the copies in flight before the CTA's shared memory goes away
+        int st = s;
+        uint32_t sp = ph;
+        const int pending = issued < kMxStages ? issued : kMxStages;
+        for (int i = 0; i < pending; ++i) {
+          if (--st < 0) {
+            st = kMxStages - 1;
+            sp ^= 1;
+          }
+          uint32_t dummy = 0;
+          mbar_wait(&full[st], sp, reinterpret_cast<volatile int*>(&dummy), P.err, 100000000ull);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ------------------------------------------------------- MMA issuer
+      int s = 0;
+      uint32_t ph = 0, acc_ph = 0;
+      bool any = false;
+      while (true) {
+        const int ti = next_tile(false);
+        if (ti < 0) break;
+        const Tile tile = P.tiles[ti];
+        const MxProblem& pr = P.prob[tile.pg >> 16];
+        const int kb = mx_kblocks(pr.K);
+        const bool two_b = GATEUP || (tile.n0 + 128 < pr.N);
+        if (!mbar_wait(acc_empty, acc_ph ^ 1, abort_flag, P.err)) break;
+        tc_fence_after_sync();
+        bool ok = true;
+        for (int ks = 0; ks < kb; ++ks) {
+          if (!mbar_wait(&full[s], ph, abort_flag, P.err) || !mbar_wait(&sf_ready[s], ph, abort_flag, P.err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const int n32 = min(4, (pr.K - ks * kMxKStage) / 32);
+          const uint32_t a_addr = smem_u32(sA + s * kMxABytes);
+          const uint32_t b_addr = smem_u32(sB + s * kMxBBytes);
+          const uint32_t cols = tmem_base + kAccCols + s * 16;
+          for (int i = 0; i < n32; ++i) {
+            // 32 K of e4m3 = 32 B per row inside the 128-byte swizzled rows; both
+            // B blocks are consecutive 128-row halves of the stage and their scale
+            // words sit at +4 and +8: one MMA of N = 256 covers both
+            umma_mxf8(tmem_base, sdesc_sw128(a_addr + i * 32, 16, 1024), sdesc_sw128(b_addr + i * 32, 16, 1024),
+                      idesc_mxf8_m128(two_b ? 256 : 128, i), cols, cols + 4, (ks | i) != 0);
+          }
+          any = true;
+          umma_commit(&empty[s]);
+          if (++s == kMxStages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (!ok) break;
+        umma_commit(acc_full);
+        acc_ph ^= 1;
+      }
+      if (any) {
+        umma_commit(drain);
+        uint32_t dummy = 0;
+        mbar_wait(drain, 0, reinterpret_cast<volatile int*>(&dummy), P.err);
+      }
+    }
+  } else if (warp >= 10) {
+    // ------------------------------------------------------- scale warps
+    // As in the NVFP4 GEMM: warps 10..13 copy a stage's atoms into its TMEM
+    // slot, each its own lane quarter (row i of an atom - 16 bytes - to lane
+    // i of every quarter). Slot s is rewritten only after full[s] completed
+    // again, i.e. after the MMAs that read it.
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    int s = 0;
+    uint32_t ph = 0;
+    while (true) {
+      const int ti = next_tile(true);
+      if (ti < 0) break;
+      const Tile tile = P.tiles[ti];
+      const MxProblem& pr = P.prob[tile.pg >> 16];
+      const int kb = mx_kblocks(pr.K);
+      const bool two_b = GATEUP || (tile.n0 + 128 < pr.N);
+      bool ok = true;
+      for (int ks = 0; ks < kb; ++ks) {
+        int got = 1;
+        if (lane == 0) got = mbar_wait(&full[s], ph, abort_flag, P.err);
+        if (!__shfl_sync(0xffffffffu, got, 0)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* sf = sSf + s * 3 * kMxSfBytes + lane * 16;
+        const uint32_t cols = tmem_base + lane_base + kAccCols + s * 16;
+        tmem_st_32x32b_x4(cols, *reinterpret_cast<const uint4*>(sf));
+        tmem_st_32x32b_x4(cols + 4, *reinterpret_cast<const uint4*>(sf + kMxSfBytes));
+        if (two_b) tmem_st_32x32b_x4(cols + 8, *reinterpret_cast<const uint4*>(sf + 2 * kMxSfBytes));
+        tmem_st_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sf_ready[s]);
+        if (++s == kMxStages) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+      if (!ok) break;
+    }
+  } else {
+    // ----------------------------------------------------------- epilogue
+    // warps 2..9: TMEM lane quarter warp % 4, column half (warp - 2) / 4;
+    // 32-column chunks j = half * 32 + 64 c, which are whole MXFP8 groups
+    const int quarter = warp & 3;
+    const int half = (warp - 2) >> 2;
+    const int r = quarter * 32 + lane;
+    uint32_t acc_ph = 0;
+    while (true) {
+      const int ti = next_tile(true);
+      if (ti < 0) break;
+      const Tile tile = P.tiles[ti];
+      const MxProblem& pr = P.prob[tile.pg >> 16];
+      const int wn = min(GATEUP ? 128 : 256, pr.N - tile.n0);
+      int got = 1;
+      if (lane == 0) got = mbar_wait(acc_full, acc_ph, abort_flag, P.err);
+      if (!__shfl_sync(0xffffffffu, got, 0)) break;
+      tc_fence_after_sync();
+      acc_ph ^= 1;
+      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+      uint32_t acc[2][32];
+      auto release_acc = [&]() {
+        tmem_ld_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty);
+      };
+      if (GATEUP) {
+        const bool valid = r < tile.rows;
+        const int grow = tile.row0 + r;
+        const int kbo = mx_kblocks(pr.N);
+        uint8_t* q = reinterpret_cast<uint8_t*>(pr.out) + static_cast<size_t>(grow) * pr.N + tile.n0;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int j = half * 32 + 64 * c;
+          if (j < wn) {
+            tmem_ld_32x32b_x32(tbase + j, acc[0]);
+            tmem_ld_32x32b_x32(tbase + 128 + j, acc[1]);
+          }
+          if (c == 1) {
+            release_acc();
+          } else {
+            tmem_ld_wait();
+          }
+          if (j >= wn) continue;
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            v[i] = gelu_tanh_exact(__uint_as_float(acc[0][i])) * __uint_as_float(acc[1][i]);
+          uint4 codes[2];
+          const uint32_t sc = mx_group(v, codes);
+          if (valid) {
+            reinterpret_cast<uint4*>(q + j)[0] = codes[0];
+            reinterpret_cast<uint4*>(q + j)[1] = codes[1];
+            pr.out_sf[mx_sf_offset(grow, (tile.n0 + j) / 32, kbo)] = static_cast<uint8_t>(sc);
+          }
+        }
+      } else {
+        // staged through the warp's buffer: whole-sector stores in row order
+        uint8_t* stg = sStg + (warp - 2) * kF4StgWarpBytes;
+        const int rows_valid = tile.rows - quarter * 32;
+        const size_t wrow = static_cast<size_t>(tile.row0 + quarter * 32);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int j = half * 32 + 64 * c;
+          if ((c & 1) == 0) {  // load chunks c, c + 1; after the second pair TMEM is no longer needed
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              if (j + 64 * u < wn) tmem_ld_32x32b_x32(tbase + j + 64 * u, acc[u]);
+            if (c == 2) {
+              release_acc();
+            } else {
+              tmem_ld_wait();
+            }
+          }
+          if (j >= wn || rows_valid <= 0) continue;
+          uint32_t* a = acc[c & 1];
+          if (pr.out_f32) {
+            uint8_t* base = reinterpret_cast<uint8_t*>(reinterpret_cast<float*>(pr.out) + wrow * pr.ldo + tile.n0 + j);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) store_rows_32B(stg, a + 8 * q, lane, base + 32 * q, pr.ldo * 4, rows_valid);
+          } else {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              pk[i] = pack_bf16x2(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
+            uint8_t* base =
+                reinterpret_cast<uint8_t*>(reinterpret_cast<__nv_bfloat16*>(pr.out) + wrow * pr.ldo + tile.n0 + j);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) store_rows_32B(stg, pk + 8 * q, lane, base + 32 * q, pr.ldo * 2, rows_valid);
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc(tmem_base, kTmemCols);
+  }
+}
+
+}  // namespace moe

@@ -11,6 +11,7 @@
 // warps in order: deterministic.
 #pragma once
 
+#include "mxformat.cuh"
 #include "ptx.cuh"
 
 namespace moe {
@@ -60,6 +61,157 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_rows_kernel(const __nv_
     for (int i = 0; i < 8; ++i) o[i] = __bfloat162float(xb[i]) * r * __bfloat162float(gb[i]);
     dst[v] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
                         pack_bf16x2(o[6], o[7]));
+  }
+}
+
+// Residual addition, RMSNorm and 8-bit output in one pass over the rows - the
+// seam between two sub-layers of the sandwich (post-norm of one, residual,
+// pre-norm of the next):
+//
+//   s[t] = residual[t] + (gamma_post x[t] / rms(x[t])  or  x[t])
+//   y[t] = gamma s[t] / rms(s[t]),   rms(v) = sqrt(mean(v^2) + eps)
+//
+// in fp32; sum = RNE_bf16(s), y = RNE_bf16(y), q / scale = MXFP8(y) from the
+// fp32 y (one rounding each). Memory bound: 4 bytes in and up to 5 + 1/32 out
+// per element, the row held in registers between the passes. A row belongs to
+// TPR threads, each with NV 8-column vectors: a warp per row up to 1024
+// columns (no block barrier, and small rows fill the warp), 128 threads up to
+// 4096, 512 up to 16384. Four neighbouring lanes hold one 32-group, so its
+// maximum takes two shuffles. Sums: a thread's squares in order, a fixed
+// xor tree, the warps in order - the same bits on every run.
+// The loads are plain (not the read-only path): sum may overwrite residual or x in place.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* s_red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (TPR > 32) {
+    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < TPR / 32; ++i) v += s_red[i];
+  }
+  return v;
+}
+
+struct AddNormParams {
+  int T, D;
+  float eps;
+  const __nv_bfloat16* x;
+  const __nv_bfloat16* residual;
+  const __nv_bfloat16* gamma_post;
+  const __nv_bfloat16* gamma;
+  __nv_bfloat16* sum;
+  __nv_bfloat16* y;
+  uint8_t* q;
+  uint8_t* scale;
+};
+
+template <int TPR, int NV>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rms_norm_kernel(const AddNormParams P) {
+  constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
+  __shared__ float s_red[2][TPR / 32];
+  pdl_wait_then_release();
+  const int lane = threadIdx.x % TPR;
+  const int t = blockIdx.x * kRows + threadIdx.x / TPR;
+  if (t >= P.T) return;  // TPR < 128 only: whole warps, no block barrier follows
+  const int nvec = P.D >> 3;
+  const size_t row = static_cast<size_t>(t) * P.D;
+  const float inv_d = 1.0f / static_cast<float>(P.D);
+  uint4 xv[NV], rv[NV];
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    const int v = lane + u * TPR;
+    xv[u] = v < nvec ? reinterpret_cast<const uint4*>(P.x + row)[v] : make_uint4(0, 0, 0, 0);
+  }
+  if (P.residual) {
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int v = lane + u * TPR;
+      rv[u] = v < nvec ? reinterpret_cast<const uint4*>(P.residual + row)[v] : make_uint4(0, 0, 0, 0);
+    }
+  }
+  float s[NV][8];
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    const __nv_bfloat16* xb = reinterpret_cast<const __nv_bfloat16*>(&xv[u]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[u][i] = __bfloat162float(xb[i]);
+  }
+  if (P.gamma_post) {
+    float ss = 0.f;
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(s[u][i], s[u][i], ss);
+    const float r = 1.0f / sqrtf(row_sum<TPR>(ss, s_red[0]) * inv_d + P.eps);
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int v = lane + u * TPR;
+      const uint4 gv =
+          v < nvec ? __ldg(reinterpret_cast<const uint4*>(P.gamma_post) + v) : make_uint4(0, 0, 0, 0);
+      const __nv_bfloat16* gb = reinterpret_cast<const __nv_bfloat16*>(&gv);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[u][i] = v < nvec ? s[u][i] * r * __bfloat162float(gb[i]) : 0.f;
+    }
+  }
+  if (P.residual) {
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const __nv_bfloat16* rb = reinterpret_cast<const __nv_bfloat16*>(&rv[u]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[u][i] += __bfloat162float(rb[i]);
+    }
+  }
+  if (P.sum) {
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int v = lane + u * TPR;
+      if (v < nvec)
+        reinterpret_cast<uint4*>(P.sum + row)[v] =
+            make_uint4(pack_bf16x2(s[u][0], s[u][1]), pack_bf16x2(s[u][2], s[u][3]), pack_bf16x2(s[u][4], s[u][5]),
+                       pack_bf16x2(s[u][6], s[u][7]));
+    }
+  }
+  if (!P.y && !P.q) return;
+  float ss = 0.f;
+#pragma unroll
+  for (int u = 0; u < NV; ++u)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(s[u][i], s[u][i], ss);
+  const float r = 1.0f / sqrtf(row_sum<TPR>(ss, s_red[1]) * inv_d + P.eps);
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    const int v = lane + u * TPR;
+    const bool in = v < nvec;
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = s[u][i] * r;
+    if (P.gamma) {
+      const uint4 gv = in ? __ldg(reinterpret_cast<const uint4*>(P.gamma) + v) : make_uint4(0, 0, 0, 0);
+      const __nv_bfloat16* gb = reinterpret_cast<const __nv_bfloat16*>(&gv);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] *= __bfloat162float(gb[i]);
+    }
+    if (P.y && in)
+      reinterpret_cast<uint4*>(P.y + row)[v] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
+                                                          pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+    if (P.q) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, abs_bits(o[i]));
+      // the four lanes of a 32-group (D is a multiple of 32: all in range, or none)
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const uint32_t sc = mx_scale_code(m);
+      const float inv = mx_inv_scale(sc);
+      if (in) {
+        reinterpret_cast<uint2*>(P.q + row)[v] =
+            make_uint2(e4m3x4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv),
+                       e4m3x4(o[4] * inv, o[5] * inv, o[6] * inv, o[7] * inv));
+        if ((v & 3) == 0) P.scale[static_cast<size_t>(t) * (P.D >> 5) + (v >> 2)] = static_cast<uint8_t>(sc);
+      }
+    }
   }
 }
 

@@ -1,0 +1,249 @@
+"""The residual-add norm and the MXFP8 block on a B200 against float64."""
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_common import SMALL, check_routing, device_weights, require_gpu, to_np, w_args, weights
+from mixture_experts_transformer_b200 import binding as B
+from mixture_experts_transformer_b200 import block, inputs
+from oracle import moe_oracle as mo
+from oracle import mxfp8 as mx
+from oracle import sandwich as sw
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def ok():
+    assert B.moe_get_device_status() == B.MOE_OK
+
+
+def dequant(q: torch.Tensor, scale: torch.Tensor) -> np.ndarray:
+    s = to_np(scale.float()).astype(np.float64)
+    return to_np(q.float()).astype(np.float64) * np.repeat(s, 32, -1)
+
+
+# ------------------------------------------------------------------ the norm
+
+# fp32 arithmetic of a row: a sum of D squares in at most D / (8 lanes' order) steps, a square root, a divide and
+# three products keep y within 2^-18 of |gamma| (|residual| + |x|) / rms for every D here (a thread adds at most 32
+# squares in order, then 5 + 16 tree steps: 53 roundings of 2^-24 on the mean, half of that on its root; the rest a
+# dozen roundings).
+FP32 = 2.0**-18
+
+
+@pytest.mark.parametrize("T,D", [(1, 8), (3, 40), (5, 256), (7, 264), (2, 1024), (9, 1032), (4, 2560), (65, 2816),
+                                 (3, 4096), (2, 4104), (3, 8192), (2, 16384)])
+@pytest.mark.parametrize("post,res,gam", [(True, True, True), (False, True, True), (False, False, False),
+                                          (True, False, True)])
+def test_add_norm(T, D, post, res, gam):
+    rng = np.random.default_rng(T * 10007 + D)
+    bits = lambda *s: inputs.f32_to_bf16_bits(rng.standard_normal(s).astype(np.float32))  # noqa: E731
+    xb, rb, gb, pb = bits(T, D), bits(T, D), bits(D), bits(D)
+    x, r, g, p = (block.bf16_tensor(b) for b in (xb, rb, gb, pb))
+    quant = D % 32 == 0
+    out = block.add_rms_norm(x, g if gam else None, residual=r if res else None, gamma_post=p if post else None,
+                             quantize=quant)
+    ok()
+    xv = mo.f64(xb)
+    a = sw.rms_norm(xv, mo.f64(pb)) if post else xv
+    rv = mo.f64(rb) if res else 0.0
+    s = rv + a
+    gv = mo.f64(gb) if gam else np.ones(D)
+    rms = np.sqrt((s * s).mean(-1, keepdims=True) + 1e-6)
+    y = gv * s / rms
+    mag = np.abs(rv) + np.abs(a)
+    es = FP32 * mag
+    # an error of s moves its row's rms by at most the largest relative one
+    ey = np.abs(gv) / rms * es + np.abs(y) * (FP32 + np.sqrt((es * es).mean(-1, keepdims=True)) / rms)
+    assert np.all(np.abs(to_np(out.sum.double()) - s) <= 2.0**-8 * np.abs(s) + es)
+    assert np.all(np.abs(to_np(out.y.double()) - y) <= 2.0**-8 * np.abs(y) + ey * 1.01)
+    if not quant:
+        return
+    got = dequant(out.q, out.scale)
+    q, j = mx.quantize(y)
+    jr = np.log2(to_np(out.scale.float()).astype(np.float64))
+    amax = np.abs(y).reshape(T, D // 32, 32).max(-1)
+    border = np.abs(amax / (448 * np.exp2(j.astype(np.float64))) - 1) < 1e-4  # the fp32 amax may pass the border
+    border |= np.abs(amax / (224 * np.exp2(j.astype(np.float64))) - 1) < 1e-4
+    assert np.all((jr == j) | border)
+    step = np.repeat(np.exp2(jr), 32, -1)
+    assert np.all(np.abs(got - y) <= np.maximum(2.0**-4 * np.abs(y), 2.0**-10 * step) + 1.07 * ey)
+    if gam:
+        assert np.mean(got != q * np.repeat(np.exp2(j.astype(np.float64)), 32, -1)) < 1e-2
+
+
+def test_add_norm_special_rows():
+    """Zero rows, a zero group, infinities and NaN, the largest and smallest values."""
+    T, D = 6, 256
+    x = torch.zeros((T, D), dtype=torch.bfloat16, device="cuda")
+    x[1, 32:64] = 3.0
+    x[2] = 1.0
+    x[2, 40] = float("inf")
+    x[3] = 1.0
+    x[3, 100] = float("nan")
+    x[4] = torch.finfo(torch.bfloat16).max / 2**70
+    x[5] = 1e-30
+    r = block.add_rms_norm(x, quantize=True)
+    ok()
+    y, q, s = r.y.float(), r.q.float(), r.scale.view(torch.uint8)
+    assert torch.equal(y[0], torch.zeros(D, device="cuda")) and torch.all(q[0] == 0) and torch.all(s[0] == 0)
+    assert torch.all(q[1, :32] == 0) and s[1, 0] == 0 and torch.all(q[1, 32:64] != 0) and torch.all(q[1, 64:] == 0)
+    assert torch.isnan(y[2, 40]) and torch.all(y[2, :40] == 0)  # inf / inf, 1 / inf
+    assert s[2, 1] == 0xFF and torch.isnan(q[2, 32:64]).all() and torch.all(q[2, :32] == 0)
+    assert torch.isnan(y[3]).all() and torch.all(s[3] == 0xFF) and torch.isnan(q[3]).all()
+    assert torch.all(y[4] == 1.0)
+    ref = 1e-30 / np.sqrt(1e-6)
+    np.testing.assert_allclose(to_np(y[5]), ref, rtol=2.0**-7)
+    # 2^-127 scales: the row's values sit below 448 2^-127 only when tiny; here they round to the nearest e4m3
+    assert torch.all(q[5] * r.scale.float()[5].repeat_interleave(32) > 0)
+
+
+def test_add_norm_in_place_and_optional_outputs():
+    T, D = 33, 2816
+    x = block.bf16_tensor(inputs.make_x(T, D, seed=5))
+    res = block.bf16_tensor(inputs.make_x(T, D, seed=6))
+    g = block.bf16_tensor(inputs.make_x(1, D, seed=7)[0])
+    ref = block.add_rms_norm(x, g, residual=res, gamma_post=g, quantize=True)
+    x2, r2 = x.clone(), res.clone()
+    got = block.add_rms_norm(x2, g, residual=r2, gamma_post=g, y=x2, sum_out=r2)
+    ok()
+    assert torch.equal(got.y, ref.y) and torch.equal(r2, ref.sum) and got.y.data_ptr() == x2.data_ptr()
+    q = torch.empty((T, D), dtype=torch.uint8, device="cuda")
+    s = torch.empty((T, D // 32), dtype=torch.uint8, device="cuda")
+    p = B.MoeNormParams(T, D, 0.0, x.data_ptr(), res.data_ptr(), g.data_ptr(), g.data_ptr(), None, None, q.data_ptr(),
+                        s.data_ptr())
+    B.check(B.moe_add_rms_norm(p), "8 bits only")
+    ok()
+    assert torch.equal(q, ref.q.view(torch.uint8)) and torch.equal(s, ref.scale.view(torch.uint8))
+    assert torch.equal(block.add_rms_norm(x[:0], g).y, x[:0])
+    with pytest.raises(ValueError):
+        block.add_rms_norm(x.t(), g)
+    with pytest.raises(ValueError):
+        block.add_rms_norm(x[:, ::2], None)
+    with pytest.raises(ValueError):
+        block.add_rms_norm(x.float(), g)
+    with pytest.raises(ValueError):
+        block.add_rms_norm(x, g[:-8])
+    with pytest.raises(ValueError):
+        block.add_rms_norm(x.cpu(), None)
+    with pytest.raises(B.MoeError):
+        block.add_rms_norm(x, g, y=x, sum_out=x)
+
+
+# ------------------------------------------------------------- quantisers
+
+
+def test_quantisers_bit_exact():
+    rng = np.random.default_rng(11)
+    G, K, N = 3, 320, 192
+    w = (rng.standard_normal((G, K, N)) * np.exp2(rng.uniform(-30, 30, (G, 1, N)))).astype(np.float32)
+    w[0, :32, 3] = 0
+    w[1, 32:64, 5] = [448.0 * 2.0**i for i in range(-16, 16)]
+    wb = inputs.f32_to_bf16_bits(w)
+    lin = block.quantize_mxfp8_linear(block.bf16_tensor(wb))
+    ok()
+    q, j = mx.quantize(np.swapaxes(mo.f64(wb), 1, 2))
+    np.testing.assert_array_equal(to_np(lin.q.float()), q)
+    sf = to_np(lin.sf.view(torch.uint8)).reshape(G, -1)
+    used = np.zeros(sf.shape[1], bool)
+    for n in range(N):
+        for c in range(K // 32):
+            o = mx.scale_tile_offset(n, c, K)
+            used[o] = True
+            np.testing.assert_array_equal(sf[:, o], j[:, n, c] + 127)
+    assert np.all(sf[:, ~used] == 0)
+    x = block.bf16_tensor(wb[0].T.copy())  # [N, K]
+    xq, xs = block.quantize_mxfp8_rows(x)
+    ok()
+    np.testing.assert_array_equal(to_np(xq.float()), q[0])
+    np.testing.assert_array_equal(to_np(xs.view(torch.uint8)), j[0] + 127)
+
+
+# ------------------------------------------------------------- the block
+
+
+def hidden_slack(xv, wg, wu):
+    """(MXFP8 GeGLU rows, how far the GPU's may be from them): an fp32 sum of K products p is within K 2^-24 sum|p| of
+    the exact one, gelu adds 2^-20 of its value (its slope is below 1.13), and a value that close to a rounding
+    border may take the neighbouring code."""
+    z, u = xv @ wg, xv @ wu
+    K = xv.shape[1]
+    dz, du = K * 2.0**-24 * (np.abs(xv) @ np.abs(wg)), K * 2.0**-24 * (np.abs(xv) @ np.abs(wu))
+    g = mo.gelu_tanh(z)
+    h = g * u
+    d = 1.13 * dz * (np.abs(u) + du) + np.abs(g) * du + 2.0**-19 * np.abs(h)
+    ref = mx.values(h)
+    near = np.maximum(np.abs(mx.values(h + d) - ref), np.abs(mx.values(h - d) - ref))
+    q, j = mx.quantize(h)
+    # a group whose largest value sits at the border of its scale may take the other scale
+    grp = np.abs(h).reshape(*h.shape[:-1], -1, 32)
+    dm = d.reshape(grp.shape).max(-1)
+    top = 448 * np.exp2(j.astype(np.float64))
+    flip = (top - grp.max(-1) < dm) | (grp.max(-1) - top / 2 < dm)
+    near = np.where(np.repeat(flip, 32, -1), np.maximum(near, 2.0**-3 * np.abs(h)), near)
+    return ref, near
+
+
+def block_reference(w, x_bits, idx, wts, xv=None):
+    """(out, bound) in float64 for a given routing. Beside the GeGLU rows' slack: fp32 sums of the down products and
+    the bf16 storage of the routed outputs (2^-8 of each, weighted)."""
+    xv = mx.values(mo.f64(x_bits)) if xv is None else xv
+
+    def ffn(rows, wg, wu, wd):
+        h, near = hidden_slack(rows, mx.weight_values(wg), mx.weight_values(wu))
+        wd = mx.weight_values(wd)
+        mag = np.abs(h) @ np.abs(wd)
+        return h @ wd, near @ np.abs(wd) + h.shape[1] * 2.0**-24 * mag
+
+    out, tol = ffn(xv, w.sg, w.su, w.sd)
+    for e in np.unique(idx):
+        t, k = np.nonzero(idx == e)
+        y, d = ffn(xv[t], w.wg[e], w.wu[e], w.wd[e])
+        wk = wts[t, k][:, None].astype(np.float64)
+        out[t] += wk * y
+        tol[t] += wk * (d + 2.0**-8 * (np.abs(y) + d) + 2.0**-20 * np.abs(y))
+    return out, tol + 2.0**-20 * np.abs(out)
+
+
+def check_block(w, x_bits, res, k, bias=None, xv=None):
+    idx, wts = to_np(res.idx), to_np(res.w)
+    ref_idx, ref_w, logits = mo.route(x_bits, w.w_router, k, bias)
+    check_routing(logits, ref_idx, ref_w, idx, wts, k)
+    out, tol = block_reference(w, x_bits, idx, wts, xv)
+    got = to_np(res.out_f32).astype(np.float64)
+    assert np.all(np.abs(got - out) <= tol), np.max(np.abs(got - out) / tol)
+    rms = np.sqrt(np.mean(out**2))
+    print("max err / rms", np.abs(got - out).max() / rms, "bound", tol.max() / rms)
+    np.testing.assert_array_equal(to_np(res.out.float()), to_np(res.out_f32.bfloat16().float()))
+    np.testing.assert_array_equal(to_np(res.cnt), np.bincount(idx.reshape(-1), minlength=w.w_router.shape[1]))
+
+
+ODD = inputs.Dims(embed_dim=320, num_experts=24, expert_dim=64, hidden_dim=448)
+
+
+@pytest.mark.parametrize("dims,T,k", [(SMALL, 17, 4), (SMALL, 130, 4), (SMALL, 300, 2), (ODD, 33, 8), (ODD, 129, 1),
+                                      (ODD, 64, 24)])
+@pytest.mark.parametrize("fed", [False, True])
+def test_block_against_oracle(dims, T, k, fed):
+    w, dw = weights(dims), device_weights(dims)
+    mw = block.quantize_mxfp8(dw)
+    xb = inputs.make_x(T, dims.embed_dim, seed=T)
+    x = block.bf16_tensor(xb)
+    xq = xs = xv = None
+    if fed:  # rows of their own, as a norm's fp32 result would give
+        rows = block.bf16_tensor(inputs.make_x(T, dims.embed_dim, seed=T + 1))
+        xq, xs = block.quantize_mxfp8_rows(rows)
+        xv = dequant(xq, xs)
+    bias = None
+    if T == 130:
+        bias = inputs.zipf_router_bias(dims.num_experts)
+    res = block.forward_mxfp8(mw, x, xq=xq, xs=xs, top_k=k, debug=True,
+                              router_bias=None if bias is None else torch.from_numpy(bias).cuda())
+    ok()
+    check_block(w, xb, res, k, bias, xv)
