@@ -482,8 +482,9 @@ def moe_block_forward_wq(p: MoeWqParams, stream=None) -> int:
     return lib().moe_block_forward_wq(ctypes.byref(p), stream_handle(stream))
 
 
-# --------------------------------------------------- MXFP8 and the add-norm
+# ----------------------------------- few tokens, MXFP8 and the add-norm
 
+FEW_MAX_TOKENS = 16
 MXFP8_GROUP = 32
 
 
@@ -510,6 +511,8 @@ class MoeMxfp8Params(ctypes.Structure):
 
 EXPORTS.update(
     {
+        "moe_few_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(MoeParams)]),
+        "moe_block_forward_few": (ctypes.c_int, [ctypes.POINTER(MoeParams), _vp]),
         "moe_add_rms_norm": (ctypes.c_int, [ctypes.POINTER(MoeNormParams), _vp]),
         "moe_mxfp8_weight_bytes": (
             ctypes.c_int,
@@ -521,6 +524,14 @@ EXPORTS.update(
         "moe_block_forward_mxfp8": (ctypes.c_int, [ctypes.POINTER(MoeMxfp8Params), _vp]),
     }
 )
+
+
+def moe_few_workspace_bytes(p: MoeParams) -> int:
+    return lib().moe_few_workspace_bytes(ctypes.byref(p))
+
+
+def moe_block_forward_few(p: MoeParams, stream=None) -> int:
+    return lib().moe_block_forward_few(ctypes.byref(p), stream_handle(stream))
 
 
 def moe_add_rms_norm(p: MoeNormParams, stream=None) -> int:

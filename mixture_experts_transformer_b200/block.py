@@ -301,7 +301,7 @@ def forward_wq(ww: WqWeights, x: torch.Tensor, *, top_k: int = B.TOP_K, router_b
     return res
 
 
-# --------------------------------------------------- MXFP8 and the add-norm
+# ----------------------------------- few tokens, MXFP8 and the add-norm
 
 
 def _rows(name: str, t: torch.Tensor, shape, dtypes, device) -> torch.Tensor:
@@ -320,6 +320,48 @@ def _on_current_device(x: torch.Tensor) -> torch.device:
 
 
 _BF16, _E4M3, _E8M0 = (torch.bfloat16,), (torch.float8_e4m3fn, torch.uint8), (torch.float8_e8m0fnu, torch.uint8)
+
+
+def few_workspace(dw: DeviceWeights, T: int, top_k: int = B.TOP_K) -> torch.Tensor:
+    """A workspace (uint8) for forward_few calls of T tokens."""
+    need = B.moe_few_workspace_bytes(B.make_params(T, top_k=top_k, dims=dw.dims))
+    return torch.empty(need, dtype=torch.uint8, device=dw.w_router.device)
+
+
+def forward_few(
+    dw: DeviceWeights,
+    x: torch.Tensor,
+    *,
+    top_k: int = B.TOP_K,
+    router_bias: torch.Tensor | None = None,
+    debug: bool = False,
+    workspace: torch.Tensor | None = None,
+    out: torch.Tensor | None = None,
+    stream=None,
+    norm_pre: torch.Tensor | None = None,
+    norm_post: torch.Tensor | None = None,
+    residual: bool = False,
+) -> BlockResult:
+    """forward() in one kernel for at most B.FEW_MAX_TOKENS tokens, unrounded between x and the output."""
+    dev = _on_current_device(x)
+    T, D = x.shape[0], dw.dims.embed_dim
+    _rows("x", x, (T, D), _BF16, dev)
+    for name, t in (("norm_pre", norm_pre), ("norm_post", norm_post)):
+        if t is not None:
+            _rows(name, t, (D,), _BF16, dev)
+    if router_bias is not None:
+        _rows("router_bias", router_bias, (dw.dims.num_experts,), (torch.float32,), dev)
+    if workspace is not None:
+        _rows("workspace", workspace, workspace.shape, (torch.uint8,), dev)
+    out = torch.empty_like(x) if out is None else _rows("out", out, (T, D), _BF16, dev)
+    res = _result(out, dw.dims, top_k, debug)
+    if debug:
+        res.logits = torch.empty((T, dw.dims.num_experts), dtype=torch.float32, device=dev)
+    p = B.make_params(T, x, *dw.args(), out, top_k=top_k, dims=dw.dims, router_bias=router_bias, out_f32=res.out_f32,
+                      idx_out=res.idx, w_out=res.w, cnt_out=res.cnt, workspace=workspace, norm_pre=norm_pre,
+                      norm_post=norm_post, residual=residual, logits_out=res.logits)
+    B.check(B.moe_block_forward_few(p, stream), "moe_block_forward_few")
+    return res
 
 
 @dataclasses.dataclass

@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "moe_block.h"
+#include "few.cuh"
 #include "grouped_gemm.cuh"
 #include "grouped_gemm_pair.cuh"
 #include "norm.cuh"
@@ -31,6 +32,8 @@ namespace {
 constexpr int kMaxDevices = 64;
 constexpr int kSmCountHint = 148;  // B200: sizes the router's split of the reduction
 constexpr size_t kAlign = 256;
+
+constexpr int kFewMaxSmem = 227 * 1024;
 
 thread_local int t_launches = 0;
 
@@ -213,6 +216,12 @@ moe_status device_state(DeviceState** out) {
       if (cudaFuncSetAttribute(fp4_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kF4SmemBytes) !=
           cudaSuccess)
         return MOE_ERR_CUDA;
+      for (const void* fn : {reinterpret_cast<const void*>(few_kernel<false, 1>),
+                             reinterpret_cast<const void*>(few_kernel<false, 2>),
+                             reinterpret_cast<const void*>(few_kernel<true, 1>),
+                             reinterpret_cast<const void*>(few_kernel<true, 2>)})
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewMaxSmem) != cudaSuccess)
+          return MOE_ERR_CUDA;
       if (cudaFuncSetAttribute(mx_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmemBytes) !=
               cudaSuccess ||
           cudaFuncSetAttribute(mx_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmemBytes) !=
@@ -339,6 +348,7 @@ enum KernelId : int {
   kKScatterMx,
   kKMxGateUp,
   kKMxDown,
+  kKFew,
   kKCount
 };
 const char* const kKernelNames[kKCount] = {"router_logits", "router_topk", "build_masks", "route_scan",
@@ -348,7 +358,7 @@ const char* const kKernelNames[kKCount] = {"router_logits", "router_topk", "buil
                                            "nvfp4_act_quant", "route_scatter_fp4", "fp4_gemm_gateup",
                                            "fp4_gemm_down", "combine_norm", "amax", "rms_norm_pre",
                                            "workspace_guard", "add_rms_norm", "route_scatter_mx", "mx_gemm_gateup",
-                                           "mx_gemm_down"};
+                                           "mx_gemm_down", "few_layer"};
 
 struct ProfRecord {
   int id;
@@ -1075,6 +1085,143 @@ moe_status enqueue_block_mx(const moe_mxfp8_params* p, const Dims& d, const MxLa
   if (p->cnt_out && cudaMemcpyAsync(p->cnt_out, cnt, d.E * 4, cudaMemcpyDeviceToDevice, st) != cudaSuccess)
     return MOE_ERR_CUDA;
   return MOE_OK;
+}
+
+// ---------------------------------------------------- the layer for a few tokens
+
+struct FewLayout {
+  size_t counters, counter_bytes, logit_part, h, part_gu, part_dn, f, guard, total;
+};
+
+bool few_fits(const Dims& d) { return d.T <= kFewMaxTokens && d.D <= kFewMaxDim && d.F <= 65536 && d.S <= 65536; }
+
+FewLayout make_few_layout(const Dims& d, bool mx) {
+  FewLayout L{};
+  const bool two = d.T > 8;
+  const size_t ntok = two ? 16 : 8;
+  const size_t kc = mx ? few_kc<true>() : few_kc<false>();
+  const size_t hc = mx ? (two ? few_hchunk<true, 2>() : few_hchunk<true, 1>())
+                       : (two ? few_hchunk<false, 2>() : few_hchunk<false, 1>());
+  const size_t act = std::min<size_t>(d.el, static_cast<size_t>(d.T) * d.k);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align_up(o + bytes, kAlign);
+    return at;
+  };
+  L.counter_bytes = (4 + d.S / 64 + static_cast<size_t>(d.el) * (d.F / 64) + (d.D + 127) / 128) * 4;
+  L.counters = take(L.counter_bytes);
+  L.logit_part = take(static_cast<size_t>((d.D + kFewRouterRows - 1) / kFewRouterRows) * 16 * 128 * 4);
+  L.h = take(((d.S + kc - 1) / kc + act * ((d.F + kc - 1) / kc)) * hc);
+  L.part_gu = take(static_cast<size_t>(kSmCountHint) * 4 * 2 * ntok * 64 * 4);
+  L.part_dn = take(static_cast<size_t>(kSmCountHint) * 2 * ntok * 128 * 4);
+  L.f = take(static_cast<size_t>(d.T) * d.D * 4);
+  L.guard = take(kGuardWords * 4);
+  L.total = o;
+  return L;
+}
+
+template <bool MX, int NT>
+cudaError_t launch_few(FewParams* P, int sm_count, cudaStream_t st) {
+  const int fixed = few_fixed_bytes<MX, NT>(P->D);
+  P->stages = std::min((kFewMaxSmem - fixed) / few_stage_bytes<MX, NT>(), kFewMaxStages);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(std::min(sm_count, kSmCountHint));
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = fixed + P->stages * few_stage_bytes<MX, NT>();
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;  // the CTAs wait on one another: all must be resident
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, few_kernel<MX, NT>, *P);
+}
+
+// Fills in the workspace pointers, clears the counters and launches. P holds the maps and the caller's pointers.
+moe_status enqueue_few(FewParams* P, const Dims& d, const FewLayout& L, uint8_t* ws, bool mx, DeviceState* s,
+                       cudaStream_t st) {
+  if (s->sm_count < kFewMaxDim / kFewRouterRows) return MOE_ERR_ARCH;
+  P->T = d.T;
+  P->k = d.k;
+  P->D = d.D;
+  P->E = d.E;
+  P->F = d.F;
+  P->S = d.S;
+  P->e0 = d.e0;
+  P->el = d.el;
+  P->counters = reinterpret_cast<uint32_t*>(ws + L.counters);
+  P->logit_part = reinterpret_cast<float*>(ws + L.logit_part);
+  P->h = ws + L.h;
+  P->part_gu = reinterpret_cast<float*>(ws + L.part_gu);
+  P->part_dn = reinterpret_cast<float*>(ws + L.part_dn);
+  P->f = reinterpret_cast<float*>(ws + L.f);
+  P->err = s->err;
+  if (cudaMemsetAsync(P->counters, 0, L.counter_bytes, st) != cudaSuccess) return MOE_ERR_CUDA;
+  LaunchScope ls_(kKFew, st);
+  const bool two = d.T > 8;
+  return ls_.done(mx ? (two ? launch_few<true, 2>(P, s->sm_count, st) : launch_few<true, 1>(P, s->sm_count, st))
+                     : (two ? launch_few<false, 2>(P, s->sm_count, st) : launch_few<false, 1>(P, s->sm_count, st)));
+}
+
+moe_status enqueue_few_bf16(const moe_params* p, const Dims& d, const FewLayout& L, uint8_t* ws, DeviceState* s,
+                            cudaStream_t st) {
+  FewParams P;
+  std::memset(&P, 0, sizeof(P));
+  if (!map_3d(&P.tmR, p->w_router, 1, d.D, d.E) || !map_3d(&P.tmG, p->wg, d.el, d.D, d.F) ||
+      !map_3d(&P.tmU, p->wu, d.el, d.D, d.F) || !map_4d_chunks(&P.tmD, p->wd, d.el, d.F, d.D, 2) ||
+      !map_3d(&P.tmSg, p->sg, 1, d.D, d.S) || !map_3d(&P.tmSu, p->su, 1, d.D, d.S) ||
+      !map_4d_chunks(&P.tmSd, p->sd, 1, d.S, d.D, 2))
+    return MOE_ERR_CUDA;
+  P.x = static_cast<const __nv_bfloat16*>(p->x);
+  P.norm_pre = static_cast<const __nv_bfloat16*>(p->norm_pre);
+  P.norm_post = static_cast<const __nv_bfloat16*>(p->norm_post);
+  P.residual = p->residual ? 1 : 0;
+  P.bias = p->router_bias;
+  P.out = static_cast<__nv_bfloat16*>(p->out);
+  P.out_f32 = p->out_f32;
+  P.idx_out = p->idx_out;
+  P.w_out = p->w_out;
+  P.cnt_out = p->cnt_out;
+  P.logits_out = p->logits_out;
+  uint32_t* guard = reinterpret_cast<uint32_t*>(ws + L.guard);
+  if (p->check_guards) {
+    LaunchScope ls_(kKGuard, st);
+    MOE_TRY(ls_.done(launch_k(guard_fill_kernel, 1, kGuardWords, 0, st, guard)));
+  }
+  MOE_TRY(enqueue_few(&P, d, L, ws, false, s, st));
+  if (p->check_guards) {
+    LaunchScope ls_(kKGuard, st);
+    MOE_TRY(ls_.done(launch_k(guard_check_kernel, 1, kGuardWords, 0, st, static_cast<const uint32_t*>(guard), s->err)));
+  }
+  return MOE_OK;
+}
+
+moe_status enqueue_few_mx(const moe_mxfp8_params* p, const Dims& d, const FewLayout& L, uint8_t* ws, DeviceState* s,
+                          cudaStream_t st) {
+  FewParams P;
+  std::memset(&P, 0, sizeof(P));
+  if (!map_3d(&P.tmR, p->w_router, 1, d.D, d.E) || !map_3d_u8(&P.tmG, p->wg.q, d.E, d.F, d.D, 64) ||
+      !map_3d_u8(&P.tmU, p->wu.q, d.E, d.F, d.D, 64) || !map_3d_u8(&P.tmD, p->wd.q, d.E, d.D, d.F) ||
+      !map_3d_u8(&P.tmSg, p->sg.q, 1, d.S, d.D, 64) || !map_3d_u8(&P.tmSu, p->su.q, 1, d.S, d.D, 64) ||
+      !map_3d_u8(&P.tmSd, p->sd.q, 1, d.D, d.S))
+    return MOE_ERR_CUDA;
+  P.sfg = p->wg.sf;
+  P.sfu = p->wu.sf;
+  P.sfd = p->wd.sf;
+  P.sfsg = p->sg.sf;
+  P.sfsu = p->su.sf;
+  P.sfsd = p->sd.sf;
+  P.x = static_cast<const __nv_bfloat16*>(p->x);
+  P.xq = static_cast<const uint8_t*>(p->xq);
+  P.xs = static_cast<const uint8_t*>(p->xs);
+  P.bias = p->router_bias;
+  P.out = static_cast<__nv_bfloat16*>(p->out);
+  P.out_f32 = p->out_f32;
+  P.idx_out = p->idx_out;
+  P.w_out = p->w_out;
+  P.cnt_out = p->cnt_out;
+  return enqueue_few(&P, d, L, ws, true, s, st);
 }
 
 template <int TPR, int NV>
@@ -1951,6 +2098,32 @@ moe_status moe_add_rms_norm(const moe_norm_params* p, void* stream) {
                                     : launch_add_norm<512, 4>(P, st));
 }
 
+size_t moe_few_workspace_bytes(const moe_params* p) {
+  if (!p) return 0;
+  const Dims d = dims_of(p);
+  if (!dims_ok(d) || !few_fits(d)) return 0;
+  return make_few_layout(d, false).total;
+}
+
+moe_status moe_block_forward_few(const moe_params* p, void* stream) {
+  ApiRange nvtx_range_("moe_block_forward_few");
+  t_launches = 0;
+  Dims d;
+  MOE_TRY(check_block_args(p, &d));
+  if (!few_fits(d)) return MOE_ERR_INVALID_ARG;
+  if (d.T == 0) return MOE_OK;
+  const size_t n = static_cast<size_t>(d.T) * d.D;
+  if (overlap(p->x, n * 2, p->out_f32, n * 4) || overlap(p->out, n * 2, p->out_f32, n * 4)) return MOE_ERR_INVALID_ARG;
+  DeviceState* s = nullptr;
+  MOE_TRY(device_state(&s));
+  if (!encode_fn()) return MOE_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const FewLayout L = make_few_layout(d, false);
+  uint8_t* ws = nullptr;
+  MOE_TRY(call_workspace(p->workspace, p->workspace_bytes, L.total, s, st, &ws));
+  return enqueue_few_bf16(p, d, L, ws, s, st);
+}
+
 moe_status moe_mxfp8_weight_bytes(int groups, int K, int N, size_t* q_bytes, size_t* sf_bytes) {
   if (groups <= 0 || K <= 0 || N <= 0 || K % 64 || N % 64) return MOE_ERR_INVALID_ARG;
   if (q_bytes) *q_bytes = mx_q_bytes(groups, K, N);
@@ -2003,7 +2176,7 @@ size_t moe_mxfp8_workspace_bytes(const moe_mxfp8_params* p) {
   if (!p) return 0;
   const Dims d = mx_dims_of(p);
   if (!dims_ok(d)) return 0;
-  return make_mx_layout(d).total;
+  return few_fits(d) ? make_few_layout(d, true).total : make_mx_layout(d).total;
 }
 
 moe_status moe_block_forward_mxfp8(const moe_mxfp8_params* p, void* stream) {
@@ -2016,8 +2189,13 @@ moe_status moe_block_forward_mxfp8(const moe_mxfp8_params* p, void* stream) {
   MOE_TRY(device_state(&s));
   if (!encode_fn()) return MOE_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const MxLayout M = make_mx_layout(d);
   uint8_t* ws = nullptr;
+  if (few_fits(d)) {
+    const FewLayout L = make_few_layout(d, true);
+    MOE_TRY(call_workspace(p->workspace, p->workspace_bytes, L.total, s, st, &ws));
+    return enqueue_few_mx(p, d, L, ws, s, st);
+  }
+  const MxLayout M = make_mx_layout(d);
   MOE_TRY(call_workspace(p->workspace, p->workspace_bytes, M.total, s, st, &ws));
   return enqueue_block_mx(p, d, M, ws, s, st);
 }
