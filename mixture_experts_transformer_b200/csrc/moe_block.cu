@@ -216,12 +216,11 @@ moe_status device_state(DeviceState** out) {
       if (cudaFuncSetAttribute(fp4_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kF4SmemBytes) !=
           cudaSuccess)
         return MOE_ERR_CUDA;
-      for (const void* fn : {reinterpret_cast<const void*>(few_kernel<false, 1>),
-                             reinterpret_cast<const void*>(few_kernel<false, 2>),
-                             reinterpret_cast<const void*>(few_kernel<true, 1>),
-                             reinterpret_cast<const void*>(few_kernel<true, 2>)})
-        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewMaxSmem) != cudaSuccess)
-          return MOE_ERR_CUDA;
+      if (cudaFuncSetAttribute(few_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewMaxSmem) !=
+              cudaSuccess ||
+          cudaFuncSetAttribute(few_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewMaxSmem) !=
+              cudaSuccess)
+        return MOE_ERR_CUDA;
       if (cudaFuncSetAttribute(mx_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmemBytes) !=
               cudaSuccess ||
           cudaFuncSetAttribute(mx_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmemBytes) !=
@@ -1093,49 +1092,50 @@ struct FewLayout {
   size_t counters, counter_bytes, logit_part, h, part_gu, part_dn, f, guard, total;
 };
 
-bool few_fits(const Dims& d) { return d.T <= kFewMaxTokens && d.D <= kFewMaxDim && d.F <= 65536 && d.S <= 65536; }
+bool few_fits(const Dims& d) {
+  return d.T <= kFewMaxTokens && d.k <= kFewMaxTopK && d.D <= kFewMaxDim && d.F <= 65536 && d.S <= 65536;
+}
 
 FewLayout make_few_layout(const Dims& d, bool mx) {
   FewLayout L{};
-  const bool two = d.T > 8;
-  const size_t ntok = two ? 16 : 8;
   const size_t kc = mx ? few_kc<true>() : few_kc<false>();
-  const size_t hc = mx ? (two ? few_hchunk<true, 2>() : few_hchunk<true, 1>())
-                       : (two ? few_hchunk<false, 2>() : few_hchunk<false, 1>());
+  const size_t hc = mx ? few_hchunk<true>(few_rows<true>(d.T)) : few_hchunk<false>(few_rows<false>(d.T));
   const size_t act = std::min<size_t>(d.el, static_cast<size_t>(d.T) * d.k);
+  auto units = [](int n, int cols) { return static_cast<size_t>((n + cols - 1) / cols); };
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
     o = align_up(o + bytes, kAlign);
     return at;
   };
-  L.counter_bytes = (4 + d.S / 64 + static_cast<size_t>(d.el) * (d.F / 64) + (d.D + 127) / 128) * 4;
+  L.counter_bytes = (4 + units(d.S, kFewGuCols) + d.el * units(d.F, kFewGuCols) + units(d.D, kFewDnCols)) * 4;
   L.counters = take(L.counter_bytes);
-  L.logit_part = take(static_cast<size_t>((d.D + kFewRouterRows - 1) / kFewRouterRows) * 16 * 128 * 4);
+  L.logit_part = take(units(d.D, kFewRouterRows) * 16 * 128 * 4);
   L.h = take(((d.S + kc - 1) / kc + act * ((d.F + kc - 1) / kc)) * hc);
-  L.part_gu = take(static_cast<size_t>(kSmCountHint) * 4 * 2 * ntok * 64 * 4);
-  L.part_dn = take(static_cast<size_t>(kSmCountHint) * 2 * ntok * 128 * 4);
+  L.part_gu = take(static_cast<size_t>(kSmCountHint) * 2 * 2 * 2 * 16 * kFewGuCols * 4);
+  L.part_dn = take(static_cast<size_t>(kSmCountHint) * 2 * 16 * kFewDnCols * 4);
   L.f = take(static_cast<size_t>(d.T) * d.D * 4);
   L.guard = take(kGuardWords * 4);
   L.total = o;
   return L;
 }
 
-template <bool MX, int NT>
+template <bool MX>
 cudaError_t launch_few(FewParams* P, int sm_count, cudaStream_t st) {
-  const int fixed = few_fixed_bytes<MX, NT>(P->D);
-  P->stages = std::min((kFewMaxSmem - fixed) / few_stage_bytes<MX, NT>(), kFewMaxStages);
+  const int rows = few_rows<MX>(P->T);
+  const int fixed = few_fixed_bytes<MX>(P->D, rows);
+  P->stages = std::min((kFewMaxSmem - fixed) / few_stage_bytes<MX>(rows), kFewMaxStages);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(std::min(sm_count, kSmCountHint));
   cfg.blockDim = dim3(kFewThreads);
-  cfg.dynamicSmemBytes = fixed + P->stages * few_stage_bytes<MX, NT>();
+  cfg.dynamicSmemBytes = fixed + P->stages * few_stage_bytes<MX>(rows);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;  // the CTAs wait on one another: all must be resident
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_kernel<MX, NT>, *P);
+  return cudaLaunchKernelEx(&cfg, few_kernel<MX>, *P);
 }
 
 // Fills in the workspace pointers, clears the counters and launches. P holds the maps and the caller's pointers.
@@ -1159,19 +1159,19 @@ moe_status enqueue_few(FewParams* P, const Dims& d, const FewLayout& L, uint8_t*
   P->err = s->err;
   if (cudaMemsetAsync(P->counters, 0, L.counter_bytes, st) != cudaSuccess) return MOE_ERR_CUDA;
   LaunchScope ls_(kKFew, st);
-  const bool two = d.T > 8;
-  return ls_.done(mx ? (two ? launch_few<true, 2>(P, s->sm_count, st) : launch_few<true, 1>(P, s->sm_count, st))
-                     : (two ? launch_few<false, 2>(P, s->sm_count, st) : launch_few<false, 1>(P, s->sm_count, st)));
+  return ls_.done(mx ? launch_few<true>(P, s->sm_count, st) : launch_few<false>(P, s->sm_count, st));
 }
 
 moe_status enqueue_few_bf16(const moe_params* p, const Dims& d, const FewLayout& L, uint8_t* ws, DeviceState* s,
                             cudaStream_t st) {
   FewParams P;
   std::memset(&P, 0, sizeof(P));
-  if (!map_3d(&P.tmR, p->w_router, 1, d.D, d.E) || !map_3d(&P.tmG, p->wg, d.el, d.D, d.F) ||
-      !map_3d(&P.tmU, p->wu, d.el, d.D, d.F) || !map_4d_chunks(&P.tmD, p->wd, d.el, d.F, d.D, 2) ||
-      !map_3d(&P.tmSg, p->sg, 1, d.D, d.S) || !map_3d(&P.tmSu, p->su, 1, d.D, d.S) ||
-      !map_4d_chunks(&P.tmSd, p->sd, 1, d.S, d.D, 2))
+  const uint32_t gu_blocks = kFewGuCols / 64, dn_blocks = kFewDnCols / 64;
+  if (!map_3d(&P.tmR, p->w_router, 1, d.D, d.E) || !map_4d_chunks(&P.tmG, p->wg, d.el, d.D, d.F, gu_blocks) ||
+      !map_4d_chunks(&P.tmU, p->wu, d.el, d.D, d.F, gu_blocks) ||
+      !map_4d_chunks(&P.tmD, p->wd, d.el, d.F, d.D, dn_blocks) ||
+      !map_4d_chunks(&P.tmSg, p->sg, 1, d.D, d.S, gu_blocks) || !map_4d_chunks(&P.tmSu, p->su, 1, d.D, d.S, gu_blocks) ||
+      !map_4d_chunks(&P.tmSd, p->sd, 1, d.S, d.D, dn_blocks))
     return MOE_ERR_CUDA;
   P.x = static_cast<const __nv_bfloat16*>(p->x);
   P.norm_pre = static_cast<const __nv_bfloat16*>(p->norm_pre);
@@ -1201,10 +1201,11 @@ moe_status enqueue_few_mx(const moe_mxfp8_params* p, const Dims& d, const FewLay
                           cudaStream_t st) {
   FewParams P;
   std::memset(&P, 0, sizeof(P));
-  if (!map_3d(&P.tmR, p->w_router, 1, d.D, d.E) || !map_3d_u8(&P.tmG, p->wg.q, d.E, d.F, d.D, 64) ||
-      !map_3d_u8(&P.tmU, p->wu.q, d.E, d.F, d.D, 64) || !map_3d_u8(&P.tmD, p->wd.q, d.E, d.D, d.F) ||
-      !map_3d_u8(&P.tmSg, p->sg.q, 1, d.S, d.D, 64) || !map_3d_u8(&P.tmSu, p->su.q, 1, d.S, d.D, 64) ||
-      !map_3d_u8(&P.tmSd, p->sd.q, 1, d.D, d.S))
+  if (!map_3d(&P.tmR, p->w_router, 1, d.D, d.E) || !map_3d_u8(&P.tmG, p->wg.q, d.E, d.F, d.D, kFewGuCols) ||
+      !map_3d_u8(&P.tmU, p->wu.q, d.E, d.F, d.D, kFewGuCols) ||
+      !map_3d_u8(&P.tmD, p->wd.q, d.E, d.D, d.F, kFewDnCols) ||
+      !map_3d_u8(&P.tmSg, p->sg.q, 1, d.S, d.D, kFewGuCols) || !map_3d_u8(&P.tmSu, p->su.q, 1, d.S, d.D, kFewGuCols) ||
+      !map_3d_u8(&P.tmSd, p->sd.q, 1, d.D, d.S, kFewDnCols))
     return MOE_ERR_CUDA;
   P.sfg = p->wg.sf;
   P.sfu = p->wu.sf;
