@@ -493,15 +493,15 @@ moe_status moe_block_forward_wq(const moe_wq_params* p, void* stream);
 
 /* --------------------------------------------- the layer for a few tokens
  *
- * moe_block_forward_ex in one kernel, for at most MOE_FEW_MAX_TOKENS tokens and
+ * moe_block_forward_ex in two kernels, for at most MOE_FEW_MAX_TOKENS tokens and
  * embed_dim <= 4096 (top_k <= 32, expert_dim and hidden_dim <= 65536): the same
  * parameters - norms, residual, expert shards, optional outputs - and the same definition,
  * but nothing between x (after norm_pre) and the output is rounded to bf16, so
  * results differ from moe_block_forward_ex's within its rounding. Bitwise
  * deterministic. workspace: at least moe_few_workspace_bytes(p) bytes, 256-byte
  * aligned, or NULL for the library's cached allocation - but not while the
- * stream is being captured, where NULL returns MOE_ERR_WORKSPACE. The kernel is
- * launched cooperatively (one CTA per SM, all resident). Calls that may run at
+ * stream is being captured, where NULL returns MOE_ERR_WORKSPACE. The second
+ * kernel is launched cooperatively (one CTA per SM, all resident). Calls that may run at
  * the same time need a workspace each.
  */
 #define MOE_FEW_MAX_TOKENS 16
@@ -585,7 +585,7 @@ moe_status moe_mxfp8_quantize_act(const void* x, int rows, int K, uint8_t* q, ui
  * the stream is being captured, where NULL returns MOE_ERR_WORKSPACE (the
  * cached allocation may be freed to grow while the graph still lives). At most
  * MOE_FEW_MAX_TOKENS tokens (with the other limits of moe_block_forward_few)
- * run as one kernel, more as grouped GEMMs.
+ * run in that form, more as grouped GEMMs.
  */
 typedef struct moe_mxfp8_params {
   int T;

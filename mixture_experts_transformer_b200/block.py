@@ -342,7 +342,7 @@ def forward_few(
     norm_post: torch.Tensor | None = None,
     residual: bool = False,
 ) -> BlockResult:
-    """forward() in one kernel for at most B.FEW_MAX_TOKENS tokens, unrounded between x and the output."""
+    """forward() in two kernels for at most B.FEW_MAX_TOKENS tokens, unrounded between x and the output."""
     dev = _on_current_device(x)
     T, D = x.shape[0], dw.dims.embed_dim
     _rows("x", x, (T, D), _BF16, dev)

@@ -1,6 +1,7 @@
-// The whole MoE layer for a few tokens (T <= 16) in one cooperative kernel:
-// router, top-k, experts, shared MLP, combine and (bf16 form) the norms and
-// residual around them.
+// The whole MoE layer for a few tokens (T <= 16) in two kernels: a small one that
+// lays x out (norm_pre, or MXFP8 quantisation), and one cooperative kernel for
+// router, top-k, experts, shared MLP, combine and (bf16 form) norm_post and
+// residual.
 //
 // A few tokens read every touched expert's weights once and compute almost
 // nothing per byte, so the layer is bound by HBM: the kernel is built as one
@@ -47,11 +48,13 @@ namespace moe {
 
 constexpr int kFewMaxTokens = 16;
 constexpr int kFewMaxTopK = 32;
-constexpr int kFewMaxDim = 4096;  // x rows stay in shared memory
-constexpr int kFewProdWarps = 4;  // one copying thread each
+constexpr int kFewMaxDim = 4096;  // at most 16 CTAs share the router's reduction
+constexpr int kFewPrepThreads = 256;
 constexpr int kFewConsWarps = 8;
+constexpr int kFewProdWarps = 4;  // copying threads 0..3, one a warp (the TMEM lane quarter of warp w is w % 4)
 constexpr int kFewMmaWarp = kFewProdWarps + 2 * kFewConsWarps;  // after 8 consumer and 8 routing warps
-constexpr int kFewThreads = 32 * (kFewMmaWarp + 1);
+constexpr int kFewProdWarp4 = kFewMmaWarp + 1;                  // copying thread 4
+constexpr int kFewThreads = 32 * (kFewMmaWarp + 2);
 constexpr int kFewWBytes = 32768;    // weights of a chunk
 constexpr int kFewSfBytes = 1024;    // MXFP8: two scale tiles of a chunk
 constexpr int kFewRouterRows = 256;  // K rows of the router per CTA (4 chunks of 64)
@@ -68,13 +71,17 @@ __host__ __device__ constexpr int few_kc() {  // K elements of a chunk: 128 byte
   return MX ? 128 : 64;
 }
 // Token rows of the MMA's B operand in memory: bf16 with at most 8 tokens keeps 8 (the other 8 columns read them
-// again through a stride of 0), which halves x in shared memory.
+// again through a stride of 0).
 template <bool MX>
 __host__ __device__ constexpr int few_rows(int T) {
   return !MX && T <= 8 ? 8 : 16;
 }
-// GeGLU rows of one K chunk of down, as the MMA's B operand: rows x 128 bytes (128-byte swizzle), bf16 high then low
-// parts; MXFP8 codes then a scale tile
+// B operand of one K chunk - x for gate|up, the GeGLU rows for down: rows x 128 bytes (128-byte swizzle); the bf16
+// GeGLU rows as high parts, then low parts; MXFP8 codes, then a scale tile
+template <bool MX>
+__host__ __device__ constexpr int few_xchunk(int rows) {
+  return MX ? rows * 128 + 512 : rows * 128;
+}
 template <bool MX>
 __host__ __device__ constexpr int few_hchunk(int rows) {
   return MX ? rows * 128 + 512 : 2 * rows * 128;
@@ -83,15 +90,9 @@ template <bool MX>
 __host__ __device__ constexpr int few_stage_bytes(int rows) {
   return kFewWBytes + (MX ? kFewSfBytes : 0) + ((few_hchunk<MX>(rows) + 1023) & ~1023);
 }
-template <bool MX>
-__host__ __device__ constexpr int few_fixed_bytes(int D, int rows) {
-  return (D + few_kc<MX>() - 1) / few_kc<MX>() * rows * 128            // x
-         + (MX ? kFewRouterRows / 64 * 16 * 128 : 0)                    // the router's bf16 slice of x
-         + (MX ? (D + 127) / 128 * 512 : 0)                             // x scale tiles
-         + 128 * 16 * 4 + 128 * 4 + 128                                 // weights, token masks, list of the touched experts
-         + kFewMaxTokens * kFewMaxTopK * 5                              // selected logits and experts
-         + kFewMaxTokens * 4 + 512 /* barriers, flags */ + 1024 /* alignment */;
-}
+constexpr int kFewFixedBytes = 128 * 16 * 4 + 128 * 4 + 128            // weights, token masks, list of the touched experts
+                               + kFewMaxTokens * kFewMaxTopK * 5         // selected logits and experts
+                               + 512 /* barriers, flags */ + 1024 /* alignment */;
 
 struct FewParams {
   CUtensorMap tmR;  // w_router [D][E] bf16, box 64 columns x 64 K
@@ -111,15 +112,17 @@ struct FewParams {
   const uint8_t* xq;  // MXFP8: the rows in 8 bits (optional)
   const uint8_t* xs;
   const __nv_bfloat16* norm_pre;
+  uint8_t* xb;  // x as B operands, one few_xchunk per K chunk
+  uint8_t* xr;  // x as the router's B operand: bf16, 64 K per block (bf16 form: xb)
   const __nv_bfloat16* norm_post;
   int residual;
   const float* bias;
-  uint32_t* counters;  // zero at launch: router, hidden, tiles done, -, then one per S unit, E unit, D tile
+  uint32_t* counters;  // cleared by few_prep_kernel: router, hidden, down, -, then one per S unit, E unit
+  int ncounters;
   float* logit_part;   // [ceil(D / 256)][16][128]
   uint8_t* h;          // GeGLU rows, one few_hchunk per K chunk of down
   float* part_gu;      // [CTA][2 phases][2][2 projections][16][128]
   float* part_dn;      // [CTA][2][16][256]
-  float* f;            // [T][D] the sums before norm_post / residual
   __nv_bfloat16* out;
   float* out_f32;
   int32_t* idx_out;
@@ -129,19 +132,21 @@ struct FewParams {
   uint32_t* err;
 };
 
-// A phase's chunk list: `units` output column blocks of `len` chunks each, cut into
-// `ctas` equal ranges (at most one CTA per chunk, so no range is empty).
+// A phase's chunk list: `units` output column blocks of `len` chunks each, cut into `ctas` ranges of base or base + 1
+// chunks (at most one CTA per chunk, so no range is empty).
 struct FewSplit {
-  long long total;
-  int len, ctas;
-  __device__ FewSplit(int units, int len_, int grid) : total(static_cast<long long>(units) * len_), len(len_) {
-    ctas = total < grid ? static_cast<int>(total) : grid;
+  int total, len, ctas, base, rem;
+  __device__ FewSplit(int units, int len_, int grid) : total(units * len_), len(len_) {
+    ctas = min(total, grid);
+    base = total / ctas;
+    rem = total - base * ctas;
   }
-  __device__ int begin(int c) const {
-    return c >= ctas ? static_cast<int>(total) : static_cast<int>(total * c / ctas);
-  }
+  __device__ int begin(int c) const { return c >= ctas ? total : c * base + min(c, rem); }
   // the CTA whose range holds chunk i
-  __device__ int cta_of(int i) const { return static_cast<int>((static_cast<long long>(i + 1) * ctas - 1) / total); }
+  __device__ int cta_of(int i) const {
+    const int big = rem * (base + 1);
+    return i < big ? i / (base + 1) : rem + (i - big) / base;
+  }
 };
 
 // ------------------------------------------------------------ small PTX pieces
@@ -209,6 +214,97 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 // Byte of (token row t, 16-byte piece p) in a block of 128-byte rows with the 128-byte swizzle.
 __device__ __forceinline__ uint32_t swz128(int t, int p) { return t * 128 + ((p ^ (t & 7)) << 4); }
 
+// x as B operands, and the counters cleared: one CTA per token. Rows past T are left as they are: a token is a
+// column of every product, and columns past T are never read.
+template <bool MX>
+__global__ void __launch_bounds__(kFewPrepThreads) few_prep_kernel(const __grid_constant__ FewParams P) {
+  __shared__ float s_red[kFewPrepThreads / 32];
+  pdl_wait_then_release();
+  const int t = blockIdx.x, tx = threadIdx.x;
+  for (int i = t * kFewPrepThreads + tx; i < P.ncounters; i += gridDim.x * kFewPrepThreads) P.counters[i] = 0;
+  const int nvec = P.D >> 3;  // 16-byte vectors of a bf16 row: at most two per thread
+  constexpr int kV = kFewMaxDim / 8 / kFewPrepThreads;
+  const int rows = few_rows<MX>(P.T);
+  uint4 xv[kV];
+#pragma unroll
+  for (int u = 0; u < kV; ++u) {
+    const int v = tx + u * kFewPrepThreads;
+    xv[u] = v < nvec ? __ldg(reinterpret_cast<const uint4*>(P.x) + static_cast<size_t>(t) * nvec + v)
+                     : make_uint4(0, 0, 0, 0);
+  }
+  if constexpr (!MX) {
+    if (P.norm_pre) {  // the same order of operations as rms_norm_rows_kernel's definition: bf16(x r gamma)
+      float ss = 0.f;
+#pragma unroll
+      for (int u = 0; u < kV; ++u) {
+        const __nv_bfloat16* xb = reinterpret_cast<const __nv_bfloat16*>(&xv[u]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(__bfloat162float(xb[i]), __bfloat162float(xb[i]), ss);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if ((tx & 31) == 0) s_red[tx >> 5] = ss;
+      __syncthreads();
+      float tot = 0.f;
+#pragma unroll
+      for (int i = 0; i < kFewPrepThreads / 32; ++i) tot += s_red[i];
+      const float r = 1.0f / sqrtf(tot / static_cast<float>(P.D) + 1e-6f);
+#pragma unroll
+      for (int u = 0; u < kV; ++u) {
+        const int v = tx + u * kFewPrepThreads;
+        const uint4 gv = v < nvec ? __ldg(reinterpret_cast<const uint4*>(P.norm_pre) + v) : make_uint4(0, 0, 0, 0);
+        const __nv_bfloat16* xb = reinterpret_cast<const __nv_bfloat16*>(&xv[u]);
+        const __nv_bfloat16* gb = reinterpret_cast<const __nv_bfloat16*>(&gv);
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = __bfloat162float(xb[j]) * r * __bfloat162float(gb[j]);
+        xv[u] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
+                           pack_bf16x2(o[6], o[7]));
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kV; ++u) {
+    const int v = tx + u * kFewPrepThreads;
+    if (v < nvec) *reinterpret_cast<uint4*>(P.xr + (v >> 3) * rows * 128 + swz128(t, v & 7)) = xv[u];
+  }
+  if constexpr (MX) {
+    const int xchunk = few_xchunk<true>(16);
+    if (P.xq) {
+      const int ng = P.D / kMxGroup;
+      for (int v = tx; v < (P.D >> 4); v += kFewPrepThreads)
+        *reinterpret_cast<uint4*>(P.xb + (v >> 3) * xchunk + swz128(t, v & 7)) =
+            __ldg(reinterpret_cast<const uint4*>(P.xq) + static_cast<size_t>(t) * (P.D >> 4) + v);
+      for (int g = tx; g < ng; g += kFewPrepThreads)
+        P.xb[(g >> 2) * xchunk + 16 * 128 + 16 * t + (g & 3)] = __ldg(P.xs + static_cast<size_t>(t) * ng + g);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kV; ++u) {  // four lanes hold a group
+        const int v = tx + u * kFewPrepThreads;
+        const __nv_bfloat16* xb = reinterpret_cast<const __nv_bfloat16*>(&xv[u]);
+        float f[8];
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          f[j] = __bfloat162float(xb[j]);
+          m = max(m, abs_bits(f[j]));
+        }
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const uint32_t sc = mx_scale_code(m);
+        const float inv = mx_inv_scale(sc);
+        if (v < nvec) {
+          uint8_t* at = P.xb + (v >> 4) * xchunk;
+          *reinterpret_cast<uint2*>(at + swz128(t, (v >> 1) & 7) + (v & 1) * 8) =
+              make_uint2(e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
+                         e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
+          if ((v & 3) == 0) at[16 * 128 + 16 * t + ((v >> 2) & 3)] = static_cast<uint8_t>(sc);
+        }
+      }
+    }
+  }
+}
+
 template <bool MX>
 __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_constant__ FewParams P) {
   constexpr int kKC = few_kc<MX>();
@@ -218,19 +314,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   const int D = P.D;
   const int rows = few_rows<MX>(P.T);
   const int stage_bytes = few_stage_bytes<MX>(rows);
-  const int hchunk = few_hchunk<MX>(rows);
+  const int hchunk = few_hchunk<MX>(rows), xchunk = few_xchunk<MX>(rows);
   const int ck = (D + kKC - 1) / kKC;  // chunks of a gate|up reduction
   uint8_t* ring = smem;
-  uint8_t* sX = ring + P.stages * stage_bytes;                    // [ck][rows][128 B], 128-byte swizzle
-  uint8_t* sXr = sX + ck * rows * 128;                            // MXFP8: [4][16][128 B] bf16
-  uint8_t* sXs = sXr + (MX ? kFewRouterRows / 64 * 16 * 128 : 0);  // MXFP8: [ck][512] scale tiles
-  float* sW = reinterpret_cast<float*>(sXs + (MX ? ck * 512 : 0));  // [list entry][16]
+  float* sW = reinterpret_cast<float*>(ring + P.stages * stage_bytes);  // [list entry][16]
   uint32_t* sBits = reinterpret_cast<uint32_t*>(sW + 128 * 16);   // [list entry] tokens routed there
   uint8_t* sList = reinterpret_cast<uint8_t*>(sBits + 128);       // [list entry] local expert
   float* sSel = reinterpret_cast<float*>(sList + 128);            // [token][slot] selected logits, then weights
   uint8_t* sCh = reinterpret_cast<uint8_t*>(sSel + kFewMaxTokens * kFewMaxTopK);  // [token][slot] selected experts
-  float* sRms = reinterpret_cast<float*>(sCh + kFewMaxTokens * kFewMaxTopK);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sRms + kFewMaxTokens);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sCh + kFewMaxTokens * kFewMaxTopK);
   uint64_t* hfull = full + kFewMaxStages;
   uint64_t* empty = hfull + kFewMaxStages;
   uint64_t* acc_full = empty + kFewMaxStages;
@@ -242,7 +334,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sTouched + 4);
   int* sCount = const_cast<int*>(abort_flag) + 1;  // touched experts
   int* sLast = sCount + 1;
-  int* sRouteOk = sCount + 2;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x, grid = gridDim.x;
@@ -252,10 +343,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   const int nd = (D + kFewDnCols - 1) / kFewDnCols;
   uint32_t* c_router = P.counters;
   uint32_t* c_hidden = P.counters + 1;
-  uint32_t* c_tiles = P.counters + 2;
+  uint32_t* c_down = P.counters + 2;
   uint32_t* c_su = P.counters + 4;
   uint32_t* c_eu = c_su + su;
-  uint32_t* c_dn = c_eu + static_cast<size_t>(P.el) * fu;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < P.stages; ++s) {
@@ -284,15 +374,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 
   const FewSplit split_s(su, ck, grid);
 
-  if (warp < kFewProdWarps) {
-    if (lane != 0 || (!MX && warp >= 2)) return;
+  if (warp < kFewProdWarps || warp == kFewProdWarp4) {
+    const int role = warp == kFewProdWarp4 ? 4 : warp;
+    if (lane != 0 || (!MX && (role == 2 || role == 3))) return;
     // --------------------------------------------------------- producers
-    // Warp 0: gate and down weights (it announces a stage's bytes on full[]);
-    // warp 1: up weights, and in D the GeGLU rows (on hfull[]); warps 2, 3
-    // (MXFP8): the scale tiles of gate | up, or of the two 128-column halves of
-    // down. Each walks the whole chunk list and waits for a stage to be free by itself; a
-    // copy may land before warp 0's announcement, the stage completes with both.
-    const int role = warp;
+    // Thread 0: gate and down weights (it announces a stage's bytes on full[]);
+    // 1: up weights; 2, 3 (MXFP8): the scale tiles of gate | up, or of the two
+    // 128-column halves of down; 4: the B operand, x or in D the GeGLU rows (on
+    // hfull[]). Each walks the whole chunk list and waits for a stage to be free by itself; a
+    // copy may land before thread 0's announcement, the stage completes with both.
     int s = 0, issued = 0;
     uint32_t ph = 0;
     bool ok = true;
@@ -311,8 +401,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     auto issue_gu = [&](const CUtensorMap* mg, const CUtensorMap* mu, const uint8_t* sg, const uint8_t* sup, int N, int g,
                         int n0, int kc) {
       uint8_t* st = ring + s * stage_bytes;
-      if (role == 0) mbar_arrive_expect_tx(&full[s], kFewWBytes + (MX ? kFewSfBytes : 0));
-      if (role < 2) {
+      if (role == 0) mbar_arrive_expect_tx(&full[s], kFewWBytes + (MX ? kFewSfBytes : 0) + xchunk);
+      if (role == 4) {
+        bulk_load(st + kHOff, P.xb + kc * xchunk, xchunk, &full[s]);
+      } else if (role < 2) {
         const CUtensorMap* m = role == 0 ? mg : mu;
         if constexpr (MX) {
           tma_load_3d(st + role * (kFewWBytes / 2), m, &full[s], kc * 128, n0, g);
@@ -336,8 +428,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     if (cta < nr) {  // the router's rows: 128 experts (two boxes of 64) x 64 K per chunk
       for (int k0 = cta * kFewRouterRows; k0 < min(D, (cta + 1) * kFewRouterRows); k0 += 64) {
         if (!acquire()) break;
-        if (role == 0) mbar_arrive_expect_tx(&full[s], 2 * 8192);
+        if (role == 0) mbar_arrive_expect_tx(&full[s], 2 * 8192 + rows * 128);
         if (role < 2) tma_load_3d(ring + s * stage_bytes + role * 8192, &P.tmR, &full[s], role * 64, k0, 0);
+        if (role == 4) bulk_load(ring + s * stage_bytes + kHOff, P.xr + k0 / 64 * rows * 128, rows * 128, &full[s]);
         advance();
       }
     }
@@ -347,7 +440,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
       advance();
     }
     if (ok && !mbar_wait(routed, 0, abort_flag, P.err)) ok = false;
-    uint32_t h_par = 0;  // per stage: the parity of its next hfull phase (role 1)
+    uint32_t h_par = 0;  // per stage: the parity of its next hfull phase (thread 4)
     int h_issued = 0;
     if (ok) {
       const int nact = *sCount;
@@ -363,7 +456,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
       const int len = ks_dn + nact * ke_dn;
       const FewSplit split_d(nd, len, grid);
       const int i0 = split_d.begin(cta), i1 = split_d.begin(cta + 1);
-      if (ok && role == 1 && i0 < i1) {
+      if (ok && role == 4 && i0 < i1) {
         // The weights of the first stages are on their way; the GeGLU rows have to be complete everywhere.
         if (!counter_wait(c_hidden, grid, abort_flag, P.err)) ok = false;
         fence_proxy_async();  // they were written by ordinary stores of other SMs
@@ -384,12 +477,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
           } else {
             tma_load_4d(st, m, &full[s], 0, kl * 64, n0 >> 6, g);
           }
-        } else if (role == 1) {
+        } else if (role == 4) {
           mbar_arrive_expect_tx(&hfull[s], hchunk);
           bulk_load(st + kHOff, P.h + static_cast<size_t>(kc) * hchunk, hchunk, &hfull[s]);
           h_par ^= 1u << s;
           ++h_issued;
-        } else if (role == 2 || two) {
+        } else if (role == 2 || (role == 3 && two)) {
           const size_t tile =
               (static_cast<size_t>(g) * ((D + 127) / 128) + (n0 >> 7) + (role - 2)) * (sh ? ks_dn : ke_dn) + kl;
           bulk_load(st + kFewWBytes + (role - 2) * 512, (sh ? P.sfsd : P.sfd) + tile * 512, 512, &full[s]);
@@ -416,17 +509,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     return;
   }
 
-  constexpr int kXThreads = 2 * 32 * kFewConsWarps;  // consumer and routing threads
   const uint32_t tmem = *tmem_slot;
 
   if (warp == kFewMmaWarp) {
     // ------------------------------------------------------- MMA issuer
-    bar_named(3, kXThreads + 32);  // x is in shared memory
     if (lane == 0) {
       int s = 0;
       uint32_t ph = 0, hph = 0, q = 0;  // q: accumulators used so far
       bool ok = true, any = false;
-      const uint32_t xa = smem_u32(sX), bsbo = rows == 8 ? 0 : 1024;
+      const uint32_t bsbo = rows == 8 ? 0 : 1024;
       auto begin_acc = [&]() -> uint32_t {  // the accumulator's first TMEM column
         if (ok && !mbar_wait(&acc_empty[q & 1], ((q >> 1) & 1) ^ 1, abort_flag, P.err)) ok = false;
         tc_fence_after_sync();
@@ -457,12 +548,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             }
             tc_fence_after_sync();
             const int kc = i % ck;
-            const uint32_t a = smem_u32(ring + s * stage_bytes), b = xa + kc * rows * 128;
+            const uint32_t a = smem_u32(ring + s * stage_bytes), b = a + kHOff;
             if constexpr (MX) {
               const uint32_t sf = tmem + kFewTmemSf + s * 16;
               tmem_cp_scales(sf, a + kFewWBytes);
               tmem_cp_scales(sf + 4, a + kFewWBytes + 512);
-              tmem_cp_scales(sf + 8, smem_u32(sXs + kc * 512));
+              tmem_cp_scales(sf + 8, b + 16 * 128);
               const int n32 = min(4, (D - kc * 128) / 32);
               for (int j = 0; j < n32; ++j) {
                 const uint64_t bd = sdesc_sw128(b + j * 32, 16, 1024);
@@ -493,11 +584,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             break;
           }
           tc_fence_after_sync();
-          const uint32_t a = smem_u32(ring + s * stage_bytes);
-          const uint32_t b = MX ? smem_u32(sXr) + (k - k0) / 64 * 2048 : xa + k / 64 * rows * 128;
+          const uint32_t a = smem_u32(ring + s * stage_bytes), b = a + kHOff;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            umma_f16(d, sdesc_sw128(a + j * 2048, 8192, 1024), sdesc_sw128(b + j * 32, 16, MX ? 1024 : bsbo),
+            umma_f16(d, sdesc_sw128(a + j * 2048, 8192, 1024), sdesc_sw128(b + j * 32, 16, bsbo),
                      few_idesc_bf16(), k != k0 || j != 0);
           end_chunk();
         }
@@ -570,117 +660,18 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     return;
   }
 
-  // ------------------------------- x into shared memory (consumer and routing warps)
   const int wx = warp - kFewProdWarps;  // 0..15
-  {
-    const int tx = wx * 32 + lane;
-    const int nvec = D >> 3;  // 16-byte vectors of a bf16 row
-    const uint4* src = reinterpret_cast<const uint4*>(P.x);
-    if constexpr (!MX) {
-      if (P.norm_pre) {
-        if (wx < P.T) {  // a row's root mean square per warp
-          float ss = 0.f;
-#pragma unroll 4
-          for (int v = lane; v < nvec; v += 32) {
-            const uint4 xv = __ldg(src + static_cast<size_t>(wx) * nvec + v);
-            const __nv_bfloat16* xb = reinterpret_cast<const __nv_bfloat16*>(&xv);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(__bfloat162float(xb[i]), __bfloat162float(xb[i]), ss);
-          }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          if (lane == 0) sRms[wx] = 1.0f / sqrtf(ss / static_cast<float>(D) + 1e-6f);
-        }
-        bar_named(5, kXThreads);
-      }
-#pragma unroll 4
-      for (int i = tx; i < rows * nvec; i += kXThreads) {
-        const int t = i / nvec, v = i - t * nvec;
-        uint4 xv = t < P.T ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-        if (P.norm_pre && t < P.T) {
-          const uint4 gv = __ldg(reinterpret_cast<const uint4*>(P.norm_pre) + v);
-          const __nv_bfloat16* xb = reinterpret_cast<const __nv_bfloat16*>(&xv);
-          const __nv_bfloat16* gb = reinterpret_cast<const __nv_bfloat16*>(&gv);
-          const float r = sRms[t];
-          float o[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = __bfloat162float(xb[j]) * r * __bfloat162float(gb[j]);
-          xv = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
-                          pack_bf16x2(o[6], o[7]));
-        }
-        *reinterpret_cast<uint4*>(sX + (v >> 3) * rows * 128 + swz128(t, v & 7)) = xv;
-      }
-    } else {
-      const int ng = D / kMxGroup;
-      // rows past T, and the scale tiles' unused bytes, are zero
-      for (int i = tx; i < ck * 32; i += kXThreads) reinterpret_cast<uint4*>(sXs)[i] = make_uint4(0, 0, 0, 0);
-      for (int i = tx; i < ck * 128; i += kXThreads)
-        if (((i >> 3) & 15) >= P.T) reinterpret_cast<uint4*>(sX)[i] = make_uint4(0, 0, 0, 0);
-      bar_named(5, kXThreads);
-      if (P.xq) {
-#pragma unroll 4
-        for (int i = tx; i < P.T * (D >> 4); i += kXThreads) {
-          const int t = i / (D >> 4), v = i - t * (D >> 4);
-          *reinterpret_cast<uint4*>(sX + (v >> 3) * 2048 + swz128(t, v & 7)) = __ldg(reinterpret_cast<const uint4*>(P.xq) + i);
-        }
-#pragma unroll 4
-        for (int i = tx; i < P.T * ng; i += kXThreads) {
-          const int t = i / ng, g = i - t * ng;
-          sXs[(g >> 2) * 512 + 16 * t + (g & 3)] = __ldg(P.xs + i);
-        }
-      } else {
-        const int items = P.T * nvec;
-#pragma unroll 2
-        for (int i0 = wx * 32; i0 < items; i0 += kXThreads) {  // four lanes hold a group
-          const int i = i0 + lane;
-          const bool in = i < items;
-          const uint4 xv = in ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-          const __nv_bfloat16* xb = reinterpret_cast<const __nv_bfloat16*>(&xv);
-          float f[8];
-          uint32_t m = 0;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            f[j] = __bfloat162float(xb[j]);
-            m = max(m, abs_bits(f[j]));
-          }
-          m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          const uint32_t sc = mx_scale_code(m);
-          const float inv = mx_inv_scale(sc);
-          if (in) {
-            const int t = i / nvec, v = i - t * nvec;  // 8 bytes of codes each
-            *reinterpret_cast<uint2*>(sX + (v >> 4) * 2048 + swz128(t, (v >> 1) & 7) + (v & 1) * 8) =
-                make_uint2(e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
-                           e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
-            if ((v & 3) == 0) sXs[(v >> 4) * 512 + 16 * t + ((v >> 2) & 3)] = static_cast<uint8_t>(sc);
-          }
-        }
-      }
-      if (cta < nr) {  // the router's bf16 columns
-        const int k0 = cta * kFewRouterRows;
-        const int nv = min(kFewRouterRows, D - k0) >> 3;
-        for (int i = tx; i < 16 * nv; i += kXThreads) {
-          const int t = i / nv, v = i - t * nv;
-          *reinterpret_cast<uint4*>(sXr + (v >> 3) * 2048 + swz128(t, v & 7)) =
-              t < P.T ? __ldg(src + static_cast<size_t>(t) * nvec + (k0 >> 3) + v) : make_uint4(0, 0, 0, 0);
-        }
-      }
-    }
-    fence_proxy_async();  // the MMAs read it
-    bar_named(3, kXThreads + 32);
-  }
-
   if (wx >= kFewConsWarps) {
     // ------------------------------------------------------------- routing
     const int wr = wx - kFewConsWarps;  // 0..7: tokens wr, wr + 8
     const int rt = wr * 32 + lane;
-    if (rt == 0) *sRouteOk = counter_wait(c_router, nr, abort_flag, P.err) ? 1 : 0;  // one poller per CTA
     for (int i = rt; i < 128 * 16; i += 256) sW[i] = 0.f;
     if (rt < 128) sBits[rt] = 0;
-    bar_named(2, 32 * kFewConsWarps);
-    const bool ok = *sRouteOk != 0;
-    if (ok) {
-      for (int t = wr; t < P.T; t += 8) {
+    if (wr < P.T) {  // warps with tokens
+      int got = 0;
+      if (lane == 0) got = counter_wait(c_router, nr, abort_flag, P.err);
+      got = __shfl_sync(0xffffffffu, got, 0);  // (a wait that gave up has raised abort)
+      for (int t = wr; t < P.T && got; t += 8) {
         // this lane's experts 4 lane .. 4 lane + 3: the partial logits in CTA order
         float l[4] = {0.f, 0.f, 0.f, 0.f};
         const int e4 = lane * 4;
@@ -745,6 +736,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
       }
     }
     bar_named(2, 32 * kFewConsWarps);
+    const bool ok = *abort_flag == 0;
     // the list of touched experts, ascending
     auto position = [&](int e) -> int {
       int pos = __popc(sTouched[e >> 5] & ((1u << (e & 31)) - 1u));
@@ -796,6 +788,17 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     if (lane == 0 && ok) mbar_arrive(&acc_empty[q & 1]);
     ++q;
   };
+  // All the warps' writes so far, seen by whoever sees the count: a barrier, then one thread's fence and atomic.
+  auto publish = [&](uint32_t* counter) -> uint32_t {
+    bar_named(1, 32 * kFewConsWarps);
+    uint32_t before = 0;
+    if (ct == 0 && ok) {
+      __threadfence();
+      before = atomicAdd(counter, 1u);
+      __threadfence();
+    }
+    return before;
+  };
   // ---- R: partial logits of 256 K rows; expert `col`, eight tokens per half
   if (cta < nr) {
     wait_acc();
@@ -807,10 +810,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
       for (int j = 0; j < 8; ++j)
         if (half * 8 + j < P.T)
           P.logit_part[(static_cast<size_t>(cta) * 16 + half * 8 + j) * 128 + col] = __uint_as_float(a[j]);
-      __threadfence();
     }
-    bar_named(1, 32 * kFewConsWarps);
-    if (ct == 0 && ok) atomicAdd(c_router, 1u);
+    publish(c_router);
   }
 
   // ---- S, E: each run of a unit's chunks leaves its sums in part_gu; the unit's last CTA makes its GeGLU rows
@@ -837,14 +838,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
           part[(16 + t) * kFewGuCols + col] = __uint_as_float(v[j]);
         }
       }
-      __threadfence();
-      bar_named(1, 32 * kFewConsWarps);
       const int ca = sp.cta_of(u * ck), cb = sp.cta_of((u + 1) * ck - 1);
-      if (ct == 0)
-        *sLast = ok && (ca == cb || atomicAdd(counters + u, 1u) == static_cast<uint32_t>(cb - ca)) ? 1 : 0;
+      const uint32_t before = publish(counters + u);
+      if (ct == 0) *sLast = ok && before == static_cast<uint32_t>(cb - ca) ? 1 : 0;
       bar_named(1, 32 * kFewConsWarps);
       if (*sLast) {
-        __threadfence();
         const int ul = u % units_per;  // unit inside its expert
         const int chunk0 = chunk_base + (u / units_per) * chunks_per;
         for (int it = ct; it < P.T * kFewGuCols; it += 256) {
@@ -857,7 +855,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             for (int c = 0; c < 8; ++c) {
               a[c] = b[c] = 0.f;
               if (c0 + c <= cb) {
-                const int sg = sp.begin(c0 + c) / ck == u ? 0 : 1;
+                const int sg = sp.begin(c0 + c) >= u * ck ? 0 : 1;  // the unit is the first of its range
                 const float* at = src + (static_cast<size_t>(c0 + c) * 4 + sg) * kUnit;
                 a[c] = __ldcg(at);
                 b[c] = __ldcg(at + 16 * kFewGuCols);
@@ -889,7 +887,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
           }
         }
         fence_proxy_async();
-        __threadfence();
       }
       bar_named(1, 32 * kFewConsWarps);  // sLast is free again, the rows are written
     }
@@ -902,11 +899,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   if (go) {
     const int nact = *sCount;
     if (nact > 0) run_gu(FewSplit(nact * fu, ck, grid), 1, fu, P.F, ks_dn, ke_dn, c_eu);
-    // run_gu ends with a barrier after every thread's rows are written and fenced
-    if (ct == 0 && ok) {
-      __threadfence();
-      atomicAdd(c_hidden, 1u);
-    }
+    publish(c_hidden);
 
     // ---- D: this thread's output column of the tile, all 16 tokens
     const int len = ks_dn + nact * ke_dn;
@@ -937,89 +930,74 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 #pragma unroll
       for (int t = 0; t < 16; ++t)
         if (t < P.T) mine[t * kFewDnCols + half * 128 + col] = tot[t];
-      __threadfence();
-      bar_named(1, 32 * kFewConsWarps);
+    }
+    publish(c_down);
+
+    // ---- the output: every CTA adds up a share of the columns (or, with norm_post or residual, whole rows), the parts
+    // in CTA order
+    if (ct == 0) *sLast = counter_wait(c_down, grid, abort_flag, P.err) ? 1 : 0;
+    bar_named(1, 32 * kFewConsWarps);
+    auto column_sum = [&](int t, int c) -> float {
+      const int u = c / kFewDnCols;
       const int ca = sp.cta_of(u * len), cb = sp.cta_of((u + 1) * len - 1);
-      if (ct == 0) *sLast = ok && atomicAdd(c_dn + u, 1u) == static_cast<uint32_t>(cb - ca) ? 1 : 0;
-      bar_named(1, 32 * kFewConsWarps);
-      if (*sLast) {  // the tile's last CTA adds the parts in CTA order
-        __threadfence();
-        const bool post = P.norm_post || P.residual;
-        for (int it = ct; it < P.T * kFewDnCols; it += 256) {
-          const int t = it / kFewDnCols, n = it % kFewDnCols;
-          const int c = u * kFewDnCols + n;
-          if (c >= D) continue;
-          const float* src = P.part_dn + t * kFewDnCols + n;
-          float a = 0.f;
-          for (int c0 = ca; c0 <= cb; c0 += 16) {
-            float b[16];
+      const float* src = P.part_dn + t * kFewDnCols + (c - u * kFewDnCols);
+      float a = 0.f;
+      for (int c0 = ca; c0 <= cb; c0 += 8) {
+        float b[8];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              b[j] = 0.f;
-              if (c0 + j <= cb)
-                b[j] = __ldcg(src + (static_cast<size_t>(c0 + j) * 2 + (sp.begin(c0 + j) / len == u ? 0 : 1)) * 16 *
-                                        kFewDnCols);
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) a += b[j];
-          }
-          const size_t at = static_cast<size_t>(t) * D + c;
-          if (post) {
-            P.f[at] = a;
-          } else {
-            if (P.out) P.out[at] = __float2bfloat16_rn(a);
-            if (P.out_f32) P.out_f32[at] = a;
-          }
+        for (int j = 0; j < 8; ++j) {
+          b[j] = 0.f;
+          if (c0 + j <= cb)
+            b[j] = __ldcg(src + (static_cast<size_t>(c0 + j) * 2 + (sp.begin(c0 + j) >= u * len ? 0 : 1)) * 16 * kFewDnCols);
         }
-        if (post) {  // norm_post needs whole rows: the CTA that finishes the last tile applies it
-          __threadfence();
-          bar_named(1, 32 * kFewConsWarps);
-          if (ct == 0) *sLast = atomicAdd(c_tiles, 1u) == static_cast<uint32_t>(nd - 1) ? 2 : 1;
-          bar_named(1, 32 * kFewConsWarps);
-          if (*sLast == 2) {
-            __threadfence();
-            for (int t = wc; t < P.T; t += 8) {
-              const float4* f = reinterpret_cast<const float4*>(P.f + static_cast<size_t>(t) * D);
-              float r = 1.f;
-              if (P.norm_post) {
-                float ss = 0.f;
-#pragma unroll 4
-                for (int v = lane; v < (D >> 2); v += 32) {
-                  const float4 a = __ldcg(f + v);
-                  ss = fmaf(a.x, a.x, fmaf(a.y, a.y, fmaf(a.z, a.z, fmaf(a.w, a.w, ss))));
-                }
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                r = 1.0f / sqrtf(ss / static_cast<float>(D) + 1e-6f);
-              }
-#pragma unroll 2
-              for (int v = lane; v < (D >> 2); v += 32) {
-                const float4 a = __ldcg(f + v);
-                float o[4] = {a.x * r, a.y * r, a.z * r, a.w * r};
-                if (P.norm_post) {
-                  const uint2 gv = __ldg(reinterpret_cast<const uint2*>(P.norm_post) + v);
-                  const __nv_bfloat16* gb = reinterpret_cast<const __nv_bfloat16*>(&gv);
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) o[j] *= __bfloat162float(gb[j]);
-                }
-                if (P.residual) {
-                  const uint2 xv = __ldg(reinterpret_cast<const uint2*>(P.x + static_cast<size_t>(t) * D) + v);
-                  const __nv_bfloat16* xb = reinterpret_cast<const __nv_bfloat16*>(&xv);
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) o[j] += __bfloat162float(xb[j]);
-                }
-                if (P.out)
-                  reinterpret_cast<uint2*>(P.out + static_cast<size_t>(t) * D)[v] =
-                      make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
-                if (P.out_f32)
-                  reinterpret_cast<float4*>(P.out_f32 + static_cast<size_t>(t) * D)[v] =
-                      make_float4(o[0], o[1], o[2], o[3]);
-              }
-            }
-          }
-        }
+        for (int j = 0; j < 8; ++j) a += b[j];
       }
-      bar_named(1, 32 * kFewConsWarps);  // sLast is free again
+      return a;
+    };
+    if (*sLast == 0) {
+      // (gave up)
+    } else if (!P.norm_post && !P.residual) {
+      const int n = P.T * D;
+      for (int it = cta * 256 + ct; it < n; it += grid * 256) {
+        const int t = it / D;
+        const float a = column_sum(t, it - t * D);
+        if (P.out) P.out[it] = __float2bfloat16_rn(a);
+        if (P.out_f32) P.out_f32[it] = a;
+      }
+    } else if (cta < P.T) {
+      constexpr int kV = kFewMaxDim / 256;
+      __shared__ float s_red[kFewConsWarps];
+      float v[kV];
+      float ss = 0.f;
+#pragma unroll
+      for (int u = 0; u < kV; ++u) {
+        const int c = ct + u * 256;
+        v[u] = c < D ? column_sum(cta, c) : 0.f;
+        ss = fmaf(v[u], v[u], ss);
+      }
+      float r = 1.f;
+      if (P.norm_post) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (lane == 0) s_red[wc] = ss;
+        bar_named(1, 32 * kFewConsWarps);
+        float tot = 0.f;
+#pragma unroll
+        for (int i = 0; i < kFewConsWarps; ++i) tot += s_red[i];
+        r = 1.0f / sqrtf(tot / static_cast<float>(D) + 1e-6f);
+      }
+#pragma unroll
+      for (int u = 0; u < kV; ++u) {
+        const int c = ct + u * 256;
+        if (c >= D) continue;
+        const size_t at = static_cast<size_t>(cta) * D + c;
+        float o = v[u] * r;
+        if (P.norm_post) o *= __bfloat162float(P.norm_post[c]);
+        if (P.residual) o += __bfloat162float(P.x[at]);
+        if (P.out) P.out[at] = __float2bfloat16_rn(o);
+        if (P.out_f32) P.out_f32[at] = o;
+      }
     }
   }
   tc_fence_before_sync();

@@ -34,6 +34,7 @@ constexpr int kSmCountHint = 148;  // B200: sizes the router's split of the redu
 constexpr size_t kAlign = 256;
 
 constexpr int kFewMaxSmem = 227 * 1024;
+constexpr int kFewStaticSmem = 64;  // few_kernel's static shared memory
 
 thread_local int t_launches = 0;
 
@@ -216,9 +217,11 @@ moe_status device_state(DeviceState** out) {
       if (cudaFuncSetAttribute(fp4_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kF4SmemBytes) !=
           cudaSuccess)
         return MOE_ERR_CUDA;
-      if (cudaFuncSetAttribute(few_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewMaxSmem) !=
+      if (cudaFuncSetAttribute(few_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kFewMaxSmem - kFewStaticSmem) !=
               cudaSuccess ||
-          cudaFuncSetAttribute(few_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewMaxSmem) !=
+          cudaFuncSetAttribute(few_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kFewMaxSmem - kFewStaticSmem) !=
               cudaSuccess)
         return MOE_ERR_CUDA;
       if (cudaFuncSetAttribute(mx_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmemBytes) !=
@@ -347,6 +350,7 @@ enum KernelId : int {
   kKScatterMx,
   kKMxGateUp,
   kKMxDown,
+  kKFewPrep,
   kKFew,
   kKCount
 };
@@ -357,7 +361,7 @@ const char* const kKernelNames[kKCount] = {"router_logits", "router_topk", "buil
                                            "nvfp4_act_quant", "route_scatter_fp4", "fp4_gemm_gateup",
                                            "fp4_gemm_down", "combine_norm", "amax", "rms_norm_pre",
                                            "workspace_guard", "add_rms_norm", "route_scatter_mx", "mx_gemm_gateup",
-                                           "mx_gemm_down", "few_layer"};
+                                           "mx_gemm_down", "few_prep", "few_layer"};
 
 struct ProfRecord {
   int id;
@@ -1089,7 +1093,8 @@ moe_status enqueue_block_mx(const moe_mxfp8_params* p, const Dims& d, const MxLa
 // ---------------------------------------------------- the layer for a few tokens
 
 struct FewLayout {
-  size_t counters, counter_bytes, logit_part, h, part_gu, part_dn, f, guard, total;
+  size_t counters, logit_part, xb, xr, h, part_gu, part_dn, guard, total;
+  int ncounters;
 };
 
 bool few_fits(const Dims& d) {
@@ -1108,13 +1113,15 @@ FewLayout make_few_layout(const Dims& d, bool mx) {
     o = align_up(o + bytes, kAlign);
     return at;
   };
-  L.counter_bytes = (4 + units(d.S, kFewGuCols) + d.el * units(d.F, kFewGuCols) + units(d.D, kFewDnCols)) * 4;
-  L.counters = take(L.counter_bytes);
+  L.ncounters = static_cast<int>(4 + units(d.S, kFewGuCols) + d.el * units(d.F, kFewGuCols));
+  L.counters = take(static_cast<size_t>(L.ncounters) * 4);
   L.logit_part = take(units(d.D, kFewRouterRows) * 16 * 128 * 4);
+  const size_t rows = mx ? few_rows<true>(d.T) : few_rows<false>(d.T);
+  L.xb = take(units(d.D, static_cast<int>(kc)) * (mx ? few_xchunk<true>(16) : rows * 128));
+  L.xr = mx ? take(static_cast<size_t>(d.D) / 64 * rows * 128) : L.xb;
   L.h = take(((d.S + kc - 1) / kc + act * ((d.F + kc - 1) / kc)) * hc);
   L.part_gu = take(static_cast<size_t>(kSmCountHint) * 2 * 2 * 2 * 16 * kFewGuCols * 4);
   L.part_dn = take(static_cast<size_t>(kSmCountHint) * 2 * 16 * kFewDnCols * 4);
-  L.f = take(static_cast<size_t>(d.T) * d.D * 4);
   L.guard = take(kGuardWords * 4);
   L.total = o;
   return L;
@@ -1123,12 +1130,11 @@ FewLayout make_few_layout(const Dims& d, bool mx) {
 template <bool MX>
 cudaError_t launch_few(FewParams* P, int sm_count, cudaStream_t st) {
   const int rows = few_rows<MX>(P->T);
-  const int fixed = few_fixed_bytes<MX>(P->D, rows);
-  P->stages = std::min((kFewMaxSmem - fixed) / few_stage_bytes<MX>(rows), kFewMaxStages);
+  P->stages = std::min((kFewMaxSmem - kFewStaticSmem - kFewFixedBytes) / few_stage_bytes<MX>(rows), kFewMaxStages);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(std::min(sm_count, kSmCountHint));
   cfg.blockDim = dim3(kFewThreads);
-  cfg.dynamicSmemBytes = fixed + P->stages * few_stage_bytes<MX>(rows);
+  cfg.dynamicSmemBytes = kFewFixedBytes + P->stages * few_stage_bytes<MX>(rows);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;  // the CTAs wait on one another: all must be resident
@@ -1138,7 +1144,7 @@ cudaError_t launch_few(FewParams* P, int sm_count, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, few_kernel<MX>, *P);
 }
 
-// Fills in the workspace pointers, clears the counters and launches. P holds the maps and the caller's pointers.
+// Fills in the workspace pointers and launches. P holds the maps and the caller's pointers.
 moe_status enqueue_few(FewParams* P, const Dims& d, const FewLayout& L, uint8_t* ws, bool mx, DeviceState* s,
                        cudaStream_t st) {
   if (s->sm_count < kFewMaxDim / kFewRouterRows) return MOE_ERR_ARCH;
@@ -1155,9 +1161,15 @@ moe_status enqueue_few(FewParams* P, const Dims& d, const FewLayout& L, uint8_t*
   P->h = ws + L.h;
   P->part_gu = reinterpret_cast<float*>(ws + L.part_gu);
   P->part_dn = reinterpret_cast<float*>(ws + L.part_dn);
-  P->f = reinterpret_cast<float*>(ws + L.f);
+  P->xb = ws + L.xb;
+  P->xr = ws + L.xr;
+  P->ncounters = L.ncounters;
   P->err = s->err;
-  if (cudaMemsetAsync(P->counters, 0, L.counter_bytes, st) != cudaSuccess) return MOE_ERR_CUDA;
+  {
+    LaunchScope ls_(kKFewPrep, st);
+    MOE_TRY(ls_.done(mx ? launch_k(few_prep_kernel<true>, d.T, kFewPrepThreads, 0, st, *P)
+                        : launch_k(few_prep_kernel<false>, d.T, kFewPrepThreads, 0, st, *P)));
+  }
   LaunchScope ls_(kKFew, st);
   return ls_.done(mx ? launch_few<true>(P, s->sm_count, st) : launch_few<false>(P, s->sm_count, st));
 }
