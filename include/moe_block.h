@@ -494,7 +494,7 @@ moe_status moe_block_forward_wq(const moe_wq_params* p, void* stream);
 /* --------------------------------------------- the layer for a few tokens
  *
  * moe_block_forward_ex in two kernels, for at most MOE_FEW_MAX_TOKENS tokens and
- * embed_dim <= 4096 (top_k <= 32, expert_dim and hidden_dim <= 65536): the same
+ * embed_dim <= 4096 (top_k <= 32, expert_dim and hidden_dim <= 16384): the same
  * parameters - norms, residual, expert shards, optional outputs - and the same definition,
  * but nothing between x (after norm_pre) and the output is rounded to bf16, so
  * results differ from moe_block_forward_ex's within its rounding. Bitwise

@@ -61,8 +61,11 @@ constexpr int kFewRouterRows = 256;  // K rows of the router per CTA (4 chunks o
 constexpr int kFewGuCols = 128;      // output columns of a gate|up chunk, per projection
 constexpr int kFewDnCols = 256;      // output columns of a down chunk
 constexpr int kFewMaxStages = 8;
-constexpr int kFewTmemCols = 256;    // two accumulators of 32 columns, then 16 columns of scales per stage
-constexpr int kFewTmemSf = 64;
+constexpr int kFewMaxCtas = 148;
+constexpr int kFewMaxHidden = 16384;  // at most 128 units of the shared MLP, fewer than CTAs
+constexpr int kFewTmemCols = 256;    // two accumulators, then (MXFP8) 16 columns of scales per stage
+constexpr int kFewTmemAcc = 64;      // columns of an accumulator: two M tiles of 16, bf16 down of up to 32 (high, low parts)
+constexpr int kFewTmemSf = 128;
 
 // ------------------------------------------------------ shared host / device sizes
 
@@ -92,6 +95,7 @@ __host__ __device__ constexpr int few_stage_bytes(int rows) {
 }
 constexpr int kFewFixedBytes = 128 * 16 * 4 + 128 * 4 + 128            // weights, token masks, list of the touched experts
                                + kFewMaxTokens * kFewMaxTopK * 5         // selected logits and experts
+                               + 3 * (kFewMaxCtas + 1) * 4 + 2 * 16 * 4  // ranges of the phases, CTAs of the output tiles
                                + 512 /* barriers, flags */ + 1024 /* alignment */;
 
 struct FewParams {
@@ -117,11 +121,12 @@ struct FewParams {
   const __nv_bfloat16* norm_post;
   int residual;
   const float* bias;
-  uint32_t* counters;  // cleared by few_prep_kernel: router, hidden, down, -, then one per S unit, E unit
+  uint32_t* counters;  // cleared by few_prep_kernel: router, hidden, down, shared, rows, then (8) one per E unit
   int ncounters;
   float* logit_part;   // [ceil(D / 256)][16][128]
   uint8_t* h;          // GeGLU rows, one few_hchunk per K chunk of down
   float* part_gu;      // [CTA][2 phases][2][2 projections][16][128]
+  float* f;            // [T][D] the sums before norm_post / residual
   float* part_dn;      // [CTA][2][16][256]
   __nv_bfloat16* out;
   float* out_f32;
@@ -132,12 +137,13 @@ struct FewParams {
   uint32_t* err;
 };
 
-// A phase's chunk list: `units` output column blocks of `len` chunks each, cut into `ctas` ranges of base or base + 1
-// chunks (at most one CTA per chunk, so no range is empty).
+// How a phase's list of `total` chunks is cut: a range of base or base + 1 chunks per CTA (at most one CTA per chunk, so
+// that no range is empty). A chunk that lies half outside its matrix counts as a whole one: it holds a ring stage as
+// long (weighting it half gave its CTAs ranges with half the bytes in flight: T = 1 48 -> 58 us).
 struct FewSplit {
-  int total, len, ctas, base, rem;
-  __device__ FewSplit(int units, int len_, int grid) : total(units * len_), len(len_) {
-    ctas = min(total, grid);
+  int total, ctas, base, rem;
+  __device__ FewSplit(int total_, int grid) : total(total_) {
+    ctas = max(1, min(total, grid));
     base = total / ctas;
     rem = total - base * ctas;
   }
@@ -161,14 +167,14 @@ __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
-// Wait until *p >= want; bounded as mbar_wait.
+// Wait until *p >= want; bounded as mbar_wait_cycles.
 __device__ __forceinline__ bool counter_wait(const uint32_t* p, uint32_t want, volatile int* abort, uint32_t* err) {
   if (ld_acquire(p) >= want) return true;
-  const uint64_t t0 = global_timer_ns();
+  const long long t0 = clock64();
   while (true) {
     if (ld_acquire(p) >= want) return true;
     if (*abort) return false;
-    if (global_timer_ns() - t0 > kWaitTimeoutNs) {
+    if (clock64() - t0 > kWaitTimeoutCycles) {
       *abort = 1;
       atomicOr(err, kErrWaitTimeout);
       return false;
@@ -195,14 +201,43 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
 // A 512-byte scale tile from shared memory into 4 TMEM columns of every lane quarter (row i of 16 bytes to lane i).
 // In order with this thread's MMAs. Descriptor: no swizzle, 8-row groups 128 bytes apart.
 __device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t saddr) {
-  const uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 32) |
-                     (static_cast<uint64_t>(1) << 46);
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+  asm volatile(
+      "{\n\t.reg .b64 a;\n\tmov.b64 a, {%1, %2};\n\ttcgen05.cp.cta_group::1.32x128b.warpx4 [%0], a;\n\t}" ::"r"(taddr),
+      "r"(saddr >> 4), "r"((128u >> 4) | (1u << 14))
+      : "memory");
 }
-// kind::f16, bf16, M = 128, N = 16, A with its M index contiguous (bit 15), B K-major.
-__host__ __device__ constexpr uint32_t few_idesc_bf16() {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (static_cast<uint32_t>(16 >> 3) << 17) |
+// kind::f16, bf16, M = 128, A with its M index contiguous (bit 15), B K-major.
+__host__ __device__ constexpr uint32_t few_idesc_bf16(int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(128 >> 4) << 24);
+}
+// The two words of an sdesc_sw128 descriptor: only the low one moves with the address (+ bytes / 16), so the MMA thread
+// adds to it instead of building 64-bit descriptors - its instruction stream is what a chunk waits for otherwise (16
+// MMAs with built descriptors took 0.6 us to issue, and a chunk 0.86 us).
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
+
+__device__ __forceinline__ void few_umma_bf16(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 a, {%1, %2};\n\t"
+      "mov.b64 b, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+      "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void few_umma_mxf8(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi,
+                                              uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 a, {%1, %2};\n\t"
+      "mov.b64 b, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.block32 [%0], a, b, %5, [%7], [%8], p;\n\t}" ::"r"(d),
+      "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+      : "memory");
 }
 
 // fp32 as an unsigned integer of the same order (a positive NaN above infinity)
@@ -322,7 +357,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   uint8_t* sList = reinterpret_cast<uint8_t*>(sBits + 128);       // [list entry] local expert
   float* sSel = reinterpret_cast<float*>(sList + 128);            // [token][slot] selected logits, then weights
   uint8_t* sCh = reinterpret_cast<uint8_t*>(sSel + kFewMaxTokens * kFewMaxTopK);  // [token][slot] selected experts
-  uint64_t* full = reinterpret_cast<uint64_t*>(sCh + kFewMaxTokens * kFewMaxTopK);
+  int* sBegS = reinterpret_cast<int*>(sCh + kFewMaxTokens * kFewMaxTopK);  // [CTA] first chunk of each range, S
+  int* sBegE = sBegS + kFewMaxCtas + 1;                                    // E
+  int* sBegD = sBegE + kFewMaxCtas + 1;                                    // D
+  int* sTileA = sBegD + kFewMaxCtas + 1;                                   // [tile] first CTA of an output tile
+  int* sTileB = sTileA + 16;                                               // [tile] last CTA
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uintptr_t>(sTileB + 16 + 1) & ~uintptr_t(7));
   uint64_t* hfull = full + kFewMaxStages;
   uint64_t* empty = hfull + kFewMaxStages;
   uint64_t* acc_full = empty + kFewMaxStages;
@@ -344,8 +384,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   uint32_t* c_router = P.counters;
   uint32_t* c_hidden = P.counters + 1;
   uint32_t* c_down = P.counters + 2;
-  uint32_t* c_su = P.counters + 4;
-  uint32_t* c_eu = c_su + su;
+  uint32_t* c_shared = P.counters + 3;
+  uint32_t* c_rows = P.counters + 4;
+  uint32_t* c_eu = P.counters + 8;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < P.stages; ++s) {
@@ -368,11 +409,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     tmem_alloc(tmem_slot, kFewTmemCols);
     tmem_relinquish();
   }
+  if (threadIdx.x <= grid) sBegS[threadIdx.x] = FewSplit(su * ck, grid).begin(threadIdx.x);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
 
-  const FewSplit split_s(su, ck, grid);
 
   if (warp < kFewProdWarps || warp == kFewProdWarp4) {
     const int role = warp == kFewProdWarp4 ? 4 : warp;
@@ -387,7 +428,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     uint32_t ph = 0;
     bool ok = true;
     auto acquire = [&]() -> bool {
-      if (!mbar_wait(&empty[s], ph ^ 1, abort_flag, P.err)) return ok = false;
+      if (!mbar_wait_cycles(&empty[s], ph ^ 1, abort_flag, P.err)) return ok = false;
       ++issued;
       return true;
     };
@@ -434,28 +475,24 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
         advance();
       }
     }
-    for (int i = split_s.begin(cta); ok && i < split_s.begin(cta + 1); ++i) {
-      if (!acquire()) break;
+    for (int i = sBegS[cta], e = sBegS[cta + 1]; i < e; ++i) {
+      if (!ok || !acquire()) break;
       issue_gu(&P.tmSg, &P.tmSu, P.sfsg, P.sfsu, P.S, 0, (i / ck) * kFewGuCols, i % ck);
       advance();
     }
-    if (ok && !mbar_wait(routed, 0, abort_flag, P.err)) ok = false;
+    if (ok && !mbar_wait_cycles(routed, 0, abort_flag, P.err)) ok = false;
     uint32_t h_par = 0;  // per stage: the parity of its next hfull phase (thread 4)
     int h_issued = 0;
     if (ok) {
       const int nact = *sCount;
-      if (nact > 0) {
-        const FewSplit split_e(nact * fu, ck, grid);
-        for (int i = split_e.begin(cta); ok && i < split_e.begin(cta + 1); ++i) {
-          if (!acquire()) break;
-          const int u = i / ck;
-          issue_gu(&P.tmG, &P.tmU, P.sfg, P.sfu, P.F, sList[u / fu], (u % fu) * kFewGuCols, i % ck);
-          advance();
-        }
+      for (int i = sBegE[cta], e = sBegE[cta + 1]; i < e; ++i) {
+        if (!acquire()) break;
+        const int u = i / ck;
+        issue_gu(&P.tmG, &P.tmU, P.sfg, P.sfu, P.F, sList[u / fu], (u % fu) * kFewGuCols, i % ck);
+        advance();
       }
       const int len = ks_dn + nact * ke_dn;
-      const FewSplit split_d(nd, len, grid);
-      const int i0 = split_d.begin(cta), i1 = split_d.begin(cta + 1);
+      const int i0 = sBegD[cta], i1 = sBegD[cta + 1];
       if (ok && role == 4 && i0 < i1) {
         // The weights of the first stages are on their way; the GeGLU rows have to be complete everywhere.
         if (!counter_wait(c_hidden, grid, abort_flag, P.err)) ok = false;
@@ -499,10 +536,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
           ph ^= 1;
         }
         uint32_t dummy = 0;
-        mbar_wait(&full[s], ph, reinterpret_cast<volatile int*>(&dummy), P.err, 100000000ull);
+        mbar_wait_cycles(&full[s], ph, reinterpret_cast<volatile int*>(&dummy), P.err, kWaitTimeoutCycles / 20);
         if (i < h_issued) {
           dummy = 0;
-          mbar_wait(&hfull[s], ((h_par >> s) & 1u) ^ 1u, reinterpret_cast<volatile int*>(&dummy), P.err, 100000000ull);
+          mbar_wait_cycles(&hfull[s], ((h_par >> s) & 1u) ^ 1u, reinterpret_cast<volatile int*>(&dummy), P.err, kWaitTimeoutCycles / 20);
         }
       }
     }
@@ -517,11 +554,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
       int s = 0;
       uint32_t ph = 0, hph = 0, q = 0;  // q: accumulators used so far
       bool ok = true, any = false;
-      const uint32_t bsbo = rows == 8 ? 0 : 1024;
+      const uint32_t xhi = desc_hi(rows == 8 ? 0 : 1024);
       auto begin_acc = [&]() -> uint32_t {  // the accumulator's first TMEM column
-        if (ok && !mbar_wait(&acc_empty[q & 1], ((q >> 1) & 1) ^ 1, abort_flag, P.err)) ok = false;
+        if (ok && !mbar_wait_cycles(&acc_empty[q & 1], ((q >> 1) & 1) ^ 1, abort_flag, P.err)) ok = false;
         tc_fence_after_sync();
-        return tmem + (q & 1) * 32;
+        return tmem + (q & 1) * kFewTmemAcc;
       };
       auto end_acc = [&]() {
         if (ok) umma_commit(&acc_full[q & 1]);
@@ -535,39 +572,45 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
           ph ^= 1;
         }
       };
+      // MXFP8: both M = 128 tiles of a chunk (accumulators d and d + n) over the K it has left (64: half a chunk)
+      auto mma_mx = [&](uint32_t d, int n, uint32_t a, uint32_t b, bool first, int k_left) {
+        const uint32_t sf = tmem + kFewTmemSf + s * 16;
+        tmem_cp_scales(sf, a + kFewWBytes);
+        tmem_cp_scales(sf + 4, a + kFewWBytes + 512);
+        tmem_cp_scales(sf + 8, b + 16 * 128);
+        const uint32_t al = desc_lo(a, 16), bl = desc_lo(b, 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j == 2 && k_left <= 64) break;
+          few_umma_mxf8(d, al + j * 2, desc_hi(1024), bl + j * 2, desc_hi(1024), idesc_mxf8_m128(16, j), sf, sf + 8,
+                        !first || j != 0);
+          few_umma_mxf8(d + n, al + kFewWBytes / 32 + j * 2, desc_hi(1024), bl + j * 2, desc_hi(1024),
+                        idesc_mxf8_m128(16, j), sf + 4, sf + 8, !first || j != 0);
+        }
+      };
       // a phase of gate|up chunks
-      auto run_gu = [&](const FewSplit& sp) {
-        const int i1 = sp.begin(cta + 1);
-        for (int i = sp.begin(cta); ok && i < i1;) {
+      auto run_gu = [&](const int* begin) {
+        const int i1 = begin[cta + 1];
+        for (int i = begin[cta]; ok && i < i1;) {
           const int iend = min(i1, (i / ck + 1) * ck);
           const uint32_t d = begin_acc();
-          for (bool first = true; ok && i < iend; ++i, first = false) {
-            if (!mbar_wait(&full[s], ph, abort_flag, P.err)) {
+          int kc = i % ck;
+          for (bool first = true; ok && i < iend; ++i, ++kc, first = false) {
+            if (!mbar_wait_cycles(&full[s], ph, abort_flag, P.err)) {
               ok = false;
               break;
             }
             tc_fence_after_sync();
-            const int kc = i % ck;
             const uint32_t a = smem_u32(ring + s * stage_bytes), b = a + kHOff;
             if constexpr (MX) {
-              const uint32_t sf = tmem + kFewTmemSf + s * 16;
-              tmem_cp_scales(sf, a + kFewWBytes);
-              tmem_cp_scales(sf + 4, a + kFewWBytes + 512);
-              tmem_cp_scales(sf + 8, b + 16 * 128);
-              const int n32 = min(4, (D - kc * 128) / 32);
-              for (int j = 0; j < n32; ++j) {
-                const uint64_t bd = sdesc_sw128(b + j * 32, 16, 1024);
-                const uint32_t acc = !first || j != 0, id = idesc_mxf8_m128(16, j);
-                umma_mxf8(d, sdesc_sw128(a + j * 32, 16, 1024), bd, id, sf, sf + 8, acc);
-                umma_mxf8(d + 16, sdesc_sw128(a + kFewWBytes / 2 + j * 32, 16, 1024), bd, id, sf + 4, sf + 8, acc);
-              }
+              mma_mx(d, 16, a, b, first, D - kc * 128);
             } else {
+              const uint32_t al = desc_lo(a, 8192), bl = desc_lo(b, 16);
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const uint64_t bd = sdesc_sw128(b + j * 32, 16, bsbo);
-                const uint32_t acc = !first || j != 0;
-                umma_f16(d, sdesc_sw128(a + j * 2048, 8192, 1024), bd, few_idesc_bf16(), acc);
-                umma_f16(d + 16, sdesc_sw128(a + kFewWBytes / 2 + j * 2048, 8192, 1024), bd, few_idesc_bf16(), acc);
+                few_umma_bf16(d, al + j * 128, desc_hi(1024), bl + j * 2, xhi, few_idesc_bf16(16), !first || j != 0);
+                few_umma_bf16(d + 16, al + kFewWBytes / 32 + j * 128, desc_hi(1024), bl + j * 2, xhi, few_idesc_bf16(16),
+                              !first || j != 0);
               }
             }
             end_chunk();
@@ -579,29 +622,28 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
         const int k0 = cta * kFewRouterRows, k1 = min(D, k0 + kFewRouterRows);
         const uint32_t d = begin_acc();
         for (int k = k0; ok && k < k1; k += 64) {
-          if (!mbar_wait(&full[s], ph, abort_flag, P.err)) {
+          if (!mbar_wait_cycles(&full[s], ph, abort_flag, P.err)) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
           const uint32_t a = smem_u32(ring + s * stage_bytes), b = a + kHOff;
+          const uint32_t al = desc_lo(a, 8192), bl = desc_lo(b, 16);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            umma_f16(d, sdesc_sw128(a + j * 2048, 8192, 1024), sdesc_sw128(b + j * 32, 16, bsbo),
-                     few_idesc_bf16(), k != k0 || j != 0);
+            few_umma_bf16(d, al + j * 128, desc_hi(1024), bl + j * 2, xhi, few_idesc_bf16(16), k != k0 || j != 0);
           end_chunk();
         }
         end_acc();
       }
-      run_gu(split_s);
-      if (ok && !mbar_wait(routed, 0, abort_flag, P.err)) ok = false;
+      run_gu(sBegS);
+      if (ok && !mbar_wait_cycles(routed, 0, abort_flag, P.err)) ok = false;
       if (ok) {
         const int nact = *sCount;
-        if (nact > 0) run_gu(FewSplit(nact * fu, ck, grid));
+        run_gu(sBegE);
         const int len = ks_dn + nact * ke_dn;
-        const FewSplit sp(nd, len, grid);
-        const int i1 = sp.begin(cta + 1);
-        for (int i = sp.begin(cta); ok && i < i1;) {  // one accumulator per run of chunks of one source
+        const int i1 = sBegD[cta + 1];
+        for (int i = sBegD[cta]; ok && i < i1;) {  // one accumulator per run of chunks of one source
           const int u = i / len;
           int kc = i - u * len;
           const int run_end = kc < ks_dn ? ks_dn : ks_dn + ((kc - ks_dn) / ke_dn + 1) * ke_dn;
@@ -610,8 +652,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
           const int K = kc < ks_dn ? P.S : P.F;
           const uint32_t d = begin_acc();
           for (bool first = true; ok && i < iend; ++i, ++kc, first = false) {
-            if (!mbar_wait(&full[s], ph, abort_flag, P.err) ||
-                !mbar_wait(&hfull[s], (hph >> s) & 1u, abort_flag, P.err)) {
+            if (!mbar_wait_cycles(&full[s], ph, abort_flag, P.err) ||
+                !mbar_wait_cycles(&hfull[s], (hph >> s) & 1u, abort_flag, P.err)) {
               ok = false;
               break;
             }
@@ -619,27 +661,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             tc_fence_after_sync();
             const uint32_t a = smem_u32(ring + s * stage_bytes), b = a + kHOff;
             if constexpr (MX) {
-              const uint32_t sf = tmem + kFewTmemSf + s * 16;
-              tmem_cp_scales(sf, a + kFewWBytes);
-              tmem_cp_scales(sf + 4, a + kFewWBytes + 512);
-              tmem_cp_scales(sf + 8, b + 16 * 128);
-              const int n32 = min(4, (K - (kc - run0) * 128) / 32);
-              for (int j = 0; j < n32; ++j) {
-                const uint64_t bd = sdesc_sw128(b + j * 32, 16, 1024);
-                const uint32_t acc = !first || j != 0, id = idesc_mxf8_m128(16, j);
-                umma_mxf8(d, sdesc_sw128(a + j * 32, 16, 1024), bd, id, sf, sf + 8, acc);
-                umma_mxf8(d + 16, sdesc_sw128(a + kFewWBytes / 2 + j * 32, 16, 1024), bd, id, sf + 4, sf + 8, acc);
-              }
+              mma_mx(d, 16, a, b, first, K - (kc - run0) * 128);
             } else {
+              // B: the high, then the low parts of the GeGLU rows, as N = 2 rows
+              const uint32_t al = desc_lo(a, 8192), bl = desc_lo(b, 16), id = few_idesc_bf16(2 * rows);
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const uint64_t hi = sdesc_sw128(b + j * 32, 16, bsbo), lo = sdesc_sw128(b + rows * 128 + j * 32, 16, bsbo);
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                  const uint64_t ad = sdesc_sw128(a + m * (kFewWBytes / 2) + j * 2048, 8192, 1024);
-                  umma_f16(d + m * 16, ad, hi, few_idesc_bf16(), !first || j != 0);
-                  umma_f16(d + m * 16, ad, lo, few_idesc_bf16(), 1);
-                }
+                few_umma_bf16(d, al + j * 128, desc_hi(1024), bl + j * 2, desc_hi(1024), id, !first || j != 0);
+                few_umma_bf16(d + 32, al + kFewWBytes / 32 + j * 128, desc_hi(1024), bl + j * 2, desc_hi(1024), id,
+                              !first || j != 0);
               }
             }
             end_chunk();
@@ -650,7 +680,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
       if (any) {
         umma_commit(drain);
         uint32_t dummy = 0;
-        mbar_wait(drain, 0, reinterpret_cast<volatile int*>(&dummy), P.err);
+        mbar_wait_cycles(drain, 0, reinterpret_cast<volatile int*>(&dummy), P.err);
       }
     }
     __syncwarp();
@@ -745,6 +775,17 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     };
     if (rt < 128 && ((sTouched[rt >> 5] >> (rt & 31)) & 1u)) sList[position(rt)] = static_cast<uint8_t>(rt - P.e0);
     if (rt == 0) *sCount = __popc(sTouched[0]) + __popc(sTouched[1]) + __popc(sTouched[2]) + __popc(sTouched[3]);
+    if (rt <= grid) {
+      const int n = __popc(sTouched[0]) + __popc(sTouched[1]) + __popc(sTouched[2]) + __popc(sTouched[3]);
+      sBegE[rt] = FewSplit(n * fu * ck, grid).begin(rt);
+      const int len = ks_dn + n * ke_dn;
+      const FewSplit sd(nd * len, grid);
+      sBegD[rt] = sd.begin(rt);
+      if (rt < nd) {
+        sTileA[rt] = sd.cta_of(rt * len);
+        sTileB[rt] = sd.cta_of((rt + 1) * len - 1);
+      }
+    }
     if (ok) {
       for (int a = rt; a < kFewMaxTokens * kFewMaxTopK; a += 256) {
         const int t = a / kFewMaxTopK, j = a % kFewMaxTopK;
@@ -777,7 +818,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   bool ok = true;
   auto wait_acc = [&]() {  // the next accumulator is complete
     int got = 0;
-    if (ok && lane == 0) got = mbar_wait(&acc_full[q & 1], (q >> 1) & 1, abort_flag, P.err);
+    if (ok && lane == 0) got = mbar_wait_cycles(&acc_full[q & 1], (q >> 1) & 1, abort_flag, P.err);
     ok = __shfl_sync(0xffffffffu, got, 0) != 0;
     tc_fence_after_sync();
   };
@@ -814,97 +855,114 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     publish(c_router);
   }
 
-  // ---- S, E: each run of a unit's chunks leaves its sums in part_gu; the unit's last CTA makes its GeGLU rows
-  auto run_gu = [&](const FewSplit& sp, int phase, int units_per, int N, int chunk_base, int chunks_per,
-                    uint32_t* counters) {
-    constexpr size_t kUnit = 2 * 16 * kFewGuCols;  // floats of a unit's partial sums
-    const int i0 = sp.begin(cta), i1 = sp.begin(cta + 1);
-    for (int i = i0; i < i1;) {
-      const int u = i / ck;
-      const int seg = u == i0 / ck ? 0 : 1;
-      // middle units (neither first nor last of the range) are whole and use the last unit's slot in turn
-      i = min(i1, (u + 1) * ck);
-      wait_acc();
-      uint32_t g[8], v[8];
-      tmem_ld_32x32b_x8(tlane + (q & 1) * 32 + half * 8, g);
-      tmem_ld_32x32b_x8(tlane + (q & 1) * 32 + 16 + half * 8, v);
-      free_acc();
-      float* part = P.part_gu + ((static_cast<size_t>(cta) * 2 + phase) * 2 + seg) * kUnit;
+  // ---- S, E: each run of a unit's chunks leaves its sums in part_gu. The shared MLP's GeGLU rows are made by all CTAs
+  // while the first experts' weights arrive; an expert unit's by its last CTA.
+  constexpr size_t kUnit = 2 * 16 * kFewGuCols;  // floats of a unit's partial sums
+  auto store_partial = [&](int phase, int seg) {
+    wait_acc();
+    uint32_t g[8], v[8];
+    tmem_ld_32x32b_x8(tlane + (q & 1) * kFewTmemAcc + half * 8, g);
+    tmem_ld_32x32b_x8(tlane + (q & 1) * kFewTmemAcc + 16 + half * 8, v);
+    free_acc();
+    float* part = P.part_gu + ((static_cast<size_t>(cta) * 2 + phase) * 2 + seg) * kUnit;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int t = half * 8 + j;
-        if (t < P.T) {
-          part[t * kFewGuCols + col] = __uint_as_float(g[j]);
-          part[(16 + t) * kFewGuCols + col] = __uint_as_float(v[j]);
-        }
+    for (int j = 0; j < 8; ++j) {
+      const int t = half * 8 + j;
+      if (t < P.T) {
+        part[t * kFewGuCols + col] = __uint_as_float(g[j]);
+        part[(16 + t) * kFewGuCols + col] = __uint_as_float(v[j]);
       }
-      const int ca = sp.cta_of(u * ck), cb = sp.cta_of((u + 1) * ck - 1);
-      const uint32_t before = publish(counters + u);
-      if (ct == 0) *sLast = ok && before == static_cast<uint32_t>(cb - ca) ? 1 : 0;
-      bar_named(1, 32 * kFewConsWarps);
-      if (*sLast) {
-        const int ul = u % units_per;  // unit inside its expert
-        const int chunk0 = chunk_base + (u / units_per) * chunks_per;
-        for (int it = ct; it < P.T * kFewGuCols; it += 256) {
-          const int t = it / kFewGuCols, n = it % kFewGuCols;
-          const float* src = P.part_gu + static_cast<size_t>(phase) * 2 * kUnit + t * kFewGuCols + n;
-          float gs = 0.f, us = 0.f;
-          for (int c0 = ca; c0 <= cb; c0 += 8) {
-            float a[8], b[8];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              a[c] = b[c] = 0.f;
-              if (c0 + c <= cb) {
-                const int sg = sp.begin(c0 + c) >= u * ck ? 0 : 1;  // the unit is the first of its range
-                const float* at = src + (static_cast<size_t>(c0 + c) * 4 + sg) * kUnit;
-                a[c] = __ldcg(at);
-                b[c] = __ldcg(at + 16 * kFewGuCols);
-              }
-            }
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              gs += a[c];
-              us += b[c];
-            }
-          }
-          const float h = gelu_tanh_exact(gs) * us;
-          const int f = ul * kFewGuCols + n;  // hidden unit of the expert
-          if constexpr (MX) {
-            const uint32_t sc = mx_scale_code(__reduce_max_sync(0xffffffffu, abs_bits(h)));  // a group per warp
-            if (f < N) {
-              uint8_t* hc = P.h + static_cast<size_t>(chunk0 + ul) * hchunk;
-              const float x = h * mx_inv_scale(sc);
-              hc[swz128(t, n >> 4) + (n & 15)] = static_cast<uint8_t>(e4m3x4(x, x, x, x) & 0xFFu);
-              if (lane == 0) hc[16 * 128 + 16 * t + (n >> 5)] = static_cast<uint8_t>(sc);
-            }
-          } else if (f < N) {
-            const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-            // an infinity or NaN stays in the high part
-            const float lo = abs_bits(__bfloat162float(hi)) >= 0x7F800000u ? 0.f : h - __bfloat162float(hi);
-            uint8_t* at = P.h + static_cast<size_t>(chunk0 + (f >> 6)) * hchunk + swz128(t, (f & 63) >> 3) + (f & 7) * 2;
-            *reinterpret_cast<__nv_bfloat16*>(at) = hi;
-            *reinterpret_cast<__nv_bfloat16*>(at + rows * 128) = __float2bfloat16_rn(lo);
-          }
-        }
-        fence_proxy_async();
-      }
-      bar_named(1, 32 * kFewConsWarps);  // sLast is free again, the rows are written
     }
   };
-  run_gu(split_s, 0, su, P.S, 0, ks_dn, c_su);
-  if (ct == 0) *sLast = mbar_wait(routed, 0, abort_flag, P.err) ? 1 : 0;
+  // The GeGLU row value of token t, column n of unit u (hidden unit f of N) from the parts of CTAs ca..cb, into the
+  // down chunks from chunk0 on. A warp's lanes hold 32 consecutive columns of one token.
+  auto finish_hidden = [&](const int* begin, int phase, int u, int ca, int cb, int t, int n, int f, int N, int chunk0) {
+    const float* src = P.part_gu + static_cast<size_t>(phase) * 2 * kUnit + t * kFewGuCols + n;
+    float gs = 0.f, us = 0.f;
+    for (int c0 = ca; c0 <= cb; c0 += 8) {
+      float a[8], b[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        a[c] = b[c] = 0.f;
+        if (c0 + c <= cb) {
+          const int sg = begin[c0 + c] >= u * ck ? 0 : 1;  // the unit is the first of its range
+          const float* at = src + (static_cast<size_t>(c0 + c) * 4 + sg) * kUnit;
+          a[c] = __ldcg(at);
+          b[c] = __ldcg(at + 16 * kFewGuCols);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        gs += a[c];
+        us += b[c];
+      }
+    }
+    const float h = gelu_tanh_exact(gs) * us;
+    if constexpr (MX) {
+      const uint32_t sc = mx_scale_code(__reduce_max_sync(0xffffffffu, abs_bits(h)));  // a group per warp
+      if (f < N) {
+        uint8_t* hc = P.h + static_cast<size_t>(chunk0 + (f >> 7)) * hchunk;
+        const float x = h * mx_inv_scale(sc);
+        hc[swz128(t, (f & 127) >> 4) + (f & 15)] = static_cast<uint8_t>(e4m3x4(x, x, x, x) & 0xFFu);
+        if (lane == 0) hc[16 * 128 + 16 * t + ((f & 127) >> 5)] = static_cast<uint8_t>(sc);
+      }
+    } else if (f < N) {
+      const __nv_bfloat16 hi = __float2bfloat16_rn(h);
+      // an infinity or NaN stays in the high part
+      const float lo = abs_bits(__bfloat162float(hi)) >= 0x7F800000u ? 0.f : h - __bfloat162float(hi);
+      uint8_t* at = P.h + static_cast<size_t>(chunk0 + (f >> 6)) * hchunk + swz128(t, (f & 63) >> 3) + (f & 7) * 2;
+      *reinterpret_cast<__nv_bfloat16*>(at) = hi;
+      *reinterpret_cast<__nv_bfloat16*>(at + rows * 128) = __float2bfloat16_rn(lo);
+    }
+  };
+  for (int i = sBegS[cta]; i < sBegS[cta + 1];) {  // at most two units: there are no more units than CTAs
+    const int u = i / ck;
+    i = min(sBegS[cta + 1], (u + 1) * ck);
+    store_partial(0, u == sBegS[cta] / ck ? 0 : 1);
+  }
+  publish(c_shared);
+  if (ct == 0)
+    *sLast = mbar_wait_cycles(routed, 0, abort_flag, P.err) && counter_wait(c_shared, grid, abort_flag, P.err) ? 1 : 0;
   bar_named(1, 32 * kFewConsWarps);
   const bool go = *sLast != 0;  // without a routing all eight warps stop here (the wait has raised abort)
   bar_named(1, 32 * kFewConsWarps);
   if (go) {
     const int nact = *sCount;
-    if (nact > 0) run_gu(FewSplit(nact * fu, ck, grid), 1, fu, P.F, ks_dn, ke_dn, c_eu);
+    const FewSplit split_s(su * ck, grid);
+    for (int it = cta * 256 + ct; it < P.T * P.S; it += grid * 256) {
+      const int t = it / P.S, f = it - t * P.S, u = f / kFewGuCols;
+      finish_hidden(sBegS, 0, u, split_s.cta_of(u * ck), split_s.cta_of((u + 1) * ck - 1), t, f % kFewGuCols, f, P.S, 0);
+    }
+    fence_proxy_async();
+    const int e0 = sBegE[cta], e1 = sBegE[cta + 1];
+    for (int i = e0; i < e1;) {
+      const int u = i / ck;
+      const int seg = u == e0 / ck ? 0 : 1;
+      // middle units (neither first nor last of the range) are whole and use the last unit's slot in turn
+      i = min(e1, (u + 1) * ck);
+      store_partial(1, seg);
+      // the CTAs that share the unit: this one's neighbours
+      int ca = cta, cb = cta;
+      while (sBegE[ca] > u * ck) --ca;
+      while (sBegE[cb + 1] < (u + 1) * ck) ++cb;
+      const uint32_t before = publish(c_eu + u);
+      if (ct == 0) *sLast = ok && before == static_cast<uint32_t>(cb - ca) ? 1 : 0;
+      bar_named(1, 32 * kFewConsWarps);
+      if (*sLast) {
+        const int e = u / fu, f0 = (u - e * fu) * kFewGuCols;
+        for (int it = ct; it < P.T * kFewGuCols; it += 256) {
+          const int n = it % kFewGuCols;
+          finish_hidden(sBegE, 1, u, ca, cb, it / kFewGuCols, n, f0 + n, P.F, ks_dn + e * ke_dn);
+        }
+        fence_proxy_async();
+      }
+      bar_named(1, 32 * kFewConsWarps);  // sLast is free again
+    }
     publish(c_hidden);
 
     // ---- D: this thread's output column of the tile, all 16 tokens
     const int len = ks_dn + nact * ke_dn;
-    const FewSplit sp(nd, len, grid);
-    const int i0 = sp.begin(cta), i1 = sp.begin(cta + 1);
+    const int i0 = sBegD[cta], i1 = sBegD[cta + 1];
     for (int i = i0; i < i1;) {
       const int u = i / len;
       const int uend = min(i1, (u + 1) * len);
@@ -915,15 +973,31 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
         const int src = kc < ks_dn ? -1 : (kc - ks_dn) / ke_dn;
         i = min(uend, u * len + ks_dn + (src + 1) * ke_dn);
         wait_acc();
-        uint32_t a[16];
-        tmem_ld_32x32b_x16(tlane + (q & 1) * 32 + half * 16, a);
-        free_acc();
+        float a[16];
+        {
+          const uint32_t at = tlane + (q & 1) * kFewTmemAcc + half * (MX ? 16 : 32);
+          uint32_t hi[16];
+          tmem_ld_32x32b_x16(at, hi);
+          if constexpr (MX) {
+            free_acc();
+#pragma unroll
+            for (int t = 0; t < 16; ++t) a[t] = __uint_as_float(hi[t]);
+          } else {  // the high and the low parts' sums: columns t and rows + t
+            uint32_t lo[16];
+            if (rows == 16) tmem_ld_32x32b_x16(at + 16, lo);
+            free_acc();
+#pragma unroll
+            for (int t = 0; t < 16; ++t)
+              a[t] = rows == 16 ? __uint_as_float(hi[t]) + __uint_as_float(lo[t])
+                                : __uint_as_float(hi[t & 7]) + __uint_as_float(hi[8 + (t & 7)]);
+          }
+        }
         if (!ok) continue;
         const uint32_t bits = src < 0 ? 0xFFFFu : sBits[src];
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
           const float w = src < 0 ? 1.f : sW[src * 16 + t];
-          if ((bits >> t) & 1u) tot[t] = fmaf(w, __uint_as_float(a[t]), tot[t]);
+          if ((bits >> t) & 1u) tot[t] = fmaf(w, a[t], tot[t]);
         }
       }
       float* mine = P.part_dn + (static_cast<size_t>(cta) * 2 + seg) * 16 * kFewDnCols;
@@ -933,13 +1007,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     }
     publish(c_down);
 
-    // ---- the output: every CTA adds up a share of the columns (or, with norm_post or residual, whole rows), the parts
-    // in CTA order
+    // ---- the output: every CTA adds up a share of the columns, the parts in CTA order
     if (ct == 0) *sLast = counter_wait(c_down, grid, abort_flag, P.err) ? 1 : 0;
     bar_named(1, 32 * kFewConsWarps);
     auto column_sum = [&](int t, int c) -> float {
       const int u = c / kFewDnCols;
-      const int ca = sp.cta_of(u * len), cb = sp.cta_of((u + 1) * len - 1);
+      const int ca = sTileA[u], cb = sTileB[u];
       const float* src = P.part_dn + t * kFewDnCols + (c - u * kFewDnCols);
       float a = 0.f;
       for (int c0 = ca; c0 <= cb; c0 += 8) {
@@ -948,7 +1021,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
         for (int j = 0; j < 8; ++j) {
           b[j] = 0.f;
           if (c0 + j <= cb)
-            b[j] = __ldcg(src + (static_cast<size_t>(c0 + j) * 2 + (sp.begin(c0 + j) >= u * len ? 0 : 1)) * 16 * kFewDnCols);
+            b[j] = __ldcg(src + (static_cast<size_t>(c0 + j) * 2 + (sBegD[c0 + j] >= u * len ? 0 : 1)) * 16 * kFewDnCols);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) a += b[j];
@@ -957,15 +1030,28 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     };
     if (*sLast == 0) {
       // (gave up)
-    } else if (!P.norm_post && !P.residual) {
+    } else {
+      const bool post = P.norm_post || P.residual;
       const int n = P.T * D;
       for (int it = cta * 256 + ct; it < n; it += grid * 256) {
         const int t = it / D;
         const float a = column_sum(t, it - t * D);
-        if (P.out) P.out[it] = __float2bfloat16_rn(a);
-        if (P.out_f32) P.out_f32[it] = a;
+        if (post) {
+          P.f[it] = a;
+        } else {
+          if (P.out) P.out[it] = __float2bfloat16_rn(a);
+          if (P.out_f32) P.out_f32[it] = a;
+        }
       }
-    } else if (cta < P.T) {
+      if (post) publish(c_rows);
+    }
+    if (*sLast != 0 && (P.norm_post || P.residual) && cta < P.T) {  // (*sLast and cta: the same for all eight warps)
+      const bool rows_ok = ct != 0 || counter_wait(c_rows, grid, abort_flag, P.err);
+      bar_named(1, 32 * kFewConsWarps);
+      if (ct == 0 && !rows_ok) *sLast = 0;
+      bar_named(1, 32 * kFewConsWarps);
+    }
+    if (*sLast != 0 && (P.norm_post || P.residual) && cta < P.T) {  // norm_post needs whole rows: a CTA each
       constexpr int kV = kFewMaxDim / 256;
       __shared__ float s_red[kFewConsWarps];
       float v[kV];
@@ -973,7 +1059,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 #pragma unroll
       for (int u = 0; u < kV; ++u) {
         const int c = ct + u * 256;
-        v[u] = c < D ? column_sum(cta, c) : 0.f;
+        v[u] = c < D ? __ldcg(P.f + static_cast<size_t>(cta) * D + c) : 0.f;
         ss = fmaf(v[u], v[u], ss);
       }
       float r = 1.f;

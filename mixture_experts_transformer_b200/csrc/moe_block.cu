@@ -1093,12 +1093,13 @@ moe_status enqueue_block_mx(const moe_mxfp8_params* p, const Dims& d, const MxLa
 // ---------------------------------------------------- the layer for a few tokens
 
 struct FewLayout {
-  size_t counters, logit_part, xb, xr, h, part_gu, part_dn, guard, total;
+  size_t counters, logit_part, xb, xr, h, part_gu, part_dn, f, guard, total;
   int ncounters;
 };
 
 bool few_fits(const Dims& d) {
-  return d.T <= kFewMaxTokens && d.k <= kFewMaxTopK && d.D <= kFewMaxDim && d.F <= 65536 && d.S <= 65536;
+  return d.T <= kFewMaxTokens && d.k <= kFewMaxTopK && d.D <= kFewMaxDim && d.F <= kFewMaxHidden &&
+         d.S <= kFewMaxHidden;
 }
 
 FewLayout make_few_layout(const Dims& d, bool mx) {
@@ -1113,15 +1114,16 @@ FewLayout make_few_layout(const Dims& d, bool mx) {
     o = align_up(o + bytes, kAlign);
     return at;
   };
-  L.ncounters = static_cast<int>(4 + units(d.S, kFewGuCols) + d.el * units(d.F, kFewGuCols));
+  L.ncounters = static_cast<int>(8 + d.el * units(d.F, kFewGuCols));
   L.counters = take(static_cast<size_t>(L.ncounters) * 4);
   L.logit_part = take(units(d.D, kFewRouterRows) * 16 * 128 * 4);
   const size_t rows = mx ? few_rows<true>(d.T) : few_rows<false>(d.T);
   L.xb = take(units(d.D, static_cast<int>(kc)) * (mx ? few_xchunk<true>(16) : rows * 128));
   L.xr = mx ? take(static_cast<size_t>(d.D) / 64 * rows * 128) : L.xb;
   L.h = take(((d.S + kc - 1) / kc + act * ((d.F + kc - 1) / kc)) * hc);
-  L.part_gu = take(static_cast<size_t>(kSmCountHint) * 2 * 2 * 2 * 16 * kFewGuCols * 4);
-  L.part_dn = take(static_cast<size_t>(kSmCountHint) * 2 * 16 * kFewDnCols * 4);
+  L.part_gu = take(static_cast<size_t>(kFewMaxCtas) * 2 * 2 * 2 * 16 * kFewGuCols * 4);
+  L.part_dn = take(static_cast<size_t>(kFewMaxCtas) * 2 * 16 * kFewDnCols * 4);
+  L.f = take(static_cast<size_t>(d.T) * d.D * 4);
   L.guard = take(kGuardWords * 4);
   L.total = o;
   return L;
@@ -1132,7 +1134,7 @@ cudaError_t launch_few(FewParams* P, int sm_count, cudaStream_t st) {
   const int rows = few_rows<MX>(P->T);
   P->stages = std::min((kFewMaxSmem - kFewStaticSmem - kFewFixedBytes) / few_stage_bytes<MX>(rows), kFewMaxStages);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(std::min(sm_count, kSmCountHint));
+  cfg.gridDim = dim3(std::min(sm_count, kFewMaxCtas));
   cfg.blockDim = dim3(kFewThreads);
   cfg.dynamicSmemBytes = kFewFixedBytes + P->stages * few_stage_bytes<MX>(rows);
   cfg.stream = st;
@@ -1147,7 +1149,7 @@ cudaError_t launch_few(FewParams* P, int sm_count, cudaStream_t st) {
 // Fills in the workspace pointers and launches. P holds the maps and the caller's pointers.
 moe_status enqueue_few(FewParams* P, const Dims& d, const FewLayout& L, uint8_t* ws, bool mx, DeviceState* s,
                        cudaStream_t st) {
-  if (s->sm_count < kFewMaxDim / kFewRouterRows) return MOE_ERR_ARCH;
+  if (s->sm_count < kFewMaxHidden / kFewGuCols) return MOE_ERR_ARCH;
   P->T = d.T;
   P->k = d.k;
   P->D = d.D;
@@ -1161,6 +1163,7 @@ moe_status enqueue_few(FewParams* P, const Dims& d, const FewLayout& L, uint8_t*
   P->h = ws + L.h;
   P->part_gu = reinterpret_cast<float*>(ws + L.part_gu);
   P->part_dn = reinterpret_cast<float*>(ws + L.part_dn);
+  P->f = reinterpret_cast<float*>(ws + L.f);
   P->xb = ws + L.xb;
   P->xr = ws + L.xr;
   P->ncounters = L.ncounters;

@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
   auto next_tile = [&](bool whole_warp) -> int {
     int ti = -1;
     if (lane == 0) {
-      if (mbar_wait(&tile_full[rs], rph, abort_flag, P.err)) {
+      if (mbar_wait_cycles(&tile_full[rs], rph, abort_flag, P.err)) {
         ti = tile_ring[rs];
         mbar_arrive(&tile_empty[rs]);
       }
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
       uint32_t ph = 0;
       int ti = atomicAdd(P.next_tile, 1);
       while (true) {
-        if (!mbar_wait(&tile_empty[rs], rph ^ 1, abort_flag, P.err)) break;
+        if (!mbar_wait_cycles(&tile_empty[rs], rph ^ 1, abort_flag, P.err)) break;
         const Tile tile = ti < num_tiles ? P.tiles[ti] : Tile{};
         const int p = tile.pg >> 16, g = tile.pg & 0xFFFF;
         bool ok = true;
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
         const uint32_t bytes = (small ? kMxASmallRows * kMxKStage : kMxABytes) +
                                (two_b ? 2 : 1) * (kMxBBytes / 2) + kMxSfBytes * (two_b ? 3 : 2);
         for (int ks = 0; ks < kb; ++ks) {
-          if (!mbar_wait(&empty[s], ph ^ 1, abort_flag, P.err)) {
+          if (!mbar_wait_cycles(&empty[s], ph ^ 1, abort_flag, P.err)) {
             ok = false;
             break;
           }
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
             sp ^= 1;
           }
           uint32_t dummy = 0;
-          mbar_wait(&full[st], sp, reinterpret_cast<volatile int*>(&dummy), P.err, 100000000ull);
+          mbar_wait_cycles(&full[st], sp, reinterpret_cast<volatile int*>(&dummy), P.err, kWaitTimeoutCycles / 20);
         }
       }
     }
@@ -388,11 +388,11 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
         const MxProblem& pr = P.prob[tile.pg >> 16];
         const int kb = mx_kblocks(pr.K);
         const bool two_b = GATEUP || (tile.n0 + 128 < pr.N);
-        if (!mbar_wait(acc_empty, acc_ph ^ 1, abort_flag, P.err)) break;
+        if (!mbar_wait_cycles(acc_empty, acc_ph ^ 1, abort_flag, P.err)) break;
         tc_fence_after_sync();
         bool ok = true;
         for (int ks = 0; ks < kb; ++ks) {
-          if (!mbar_wait(&full[s], ph, abort_flag, P.err) || !mbar_wait(&sf_ready[s], ph, abort_flag, P.err)) {
+          if (!mbar_wait_cycles(&full[s], ph, abort_flag, P.err) || !mbar_wait_cycles(&sf_ready[s], ph, abort_flag, P.err)) {
             ok = false;
             break;
           }
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
       if (any) {
         umma_commit(drain);
         uint32_t dummy = 0;
-        mbar_wait(drain, 0, reinterpret_cast<volatile int*>(&dummy), P.err);
+        mbar_wait_cycles(drain, 0, reinterpret_cast<volatile int*>(&dummy), P.err);
       }
     }
   } else if (warp >= 10) {
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
       bool ok = true;
       for (int ks = 0; ks < kb; ++ks) {
         int got = 1;
-        if (lane == 0) got = mbar_wait(&full[s], ph, abort_flag, P.err);
+        if (lane == 0) got = mbar_wait_cycles(&full[s], ph, abort_flag, P.err);
         if (!__shfl_sync(0xffffffffu, got, 0)) {
           ok = false;
           break;
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
       const MxProblem& pr = P.prob[tile.pg >> 16];
       const int wn = min(GATEUP ? 128 : 256, pr.N - tile.n0);
       int got = 1;
-      if (lane == 0) got = mbar_wait(acc_full, acc_ph, abort_flag, P.err);
+      if (lane == 0) got = mbar_wait_cycles(acc_full, acc_ph, abort_flag, P.err);
       if (!__shfl_sync(0xffffffffu, got, 0)) break;
       tc_fence_after_sync();
       acc_ph ^= 1;

@@ -81,6 +81,27 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// mbar_wait with its limit taken from the SM's cycle counter. Reading
+// %globaltimer takes long enough (most of a microsecond) that a thread whose
+// barrier completes meanwhile notices late: the few-token kernel's chunk period
+// was 0.86 us with mbar_wait, whatever the chunk held.
+constexpr long long kWaitTimeoutCycles = 4000000000ll;  // about 2 s at 1.9 GHz
+
+__device__ __forceinline__ bool mbar_wait_cycles(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err,
+                                                 long long timeout_cycles = kWaitTimeoutCycles) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (clock64() - t0 > timeout_cycles) {
+      *abort = 1;
+      atomicOr(err, kErrWaitTimeout);
+      return false;
+    }
+  }
+}
+
 // ------------------------------------------------------- dependent launch
 
 // Programmatic dependent launch: wait until the previous kernel in the stream
