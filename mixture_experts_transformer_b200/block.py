@@ -306,7 +306,7 @@ def forward_wq(ww: WqWeights, x: torch.Tensor, *, top_k: int = B.TOP_K, router_b
 
 def _rows(name: str, t: torch.Tensor, shape, dtypes, device) -> torch.Tensor:
     """t itself, after checking that it is a contiguous [shape] tensor of one of `dtypes` on `device`."""
-    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype not in dtypes or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: needs a contiguous {tuple(shape)} tensor of {' or '.join(map(str, dtypes))} on "
                          f"{device}, got {tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
     return t
@@ -357,9 +357,12 @@ def forward_few(
     res = _result(out, dw.dims, top_k, debug)
     if debug:
         res.logits = torch.empty((T, dw.dims.num_experts), dtype=torch.float32, device=dev)
-    p = B.make_params(T, x, *dw.args(), out, top_k=top_k, dims=dw.dims, router_bias=router_bias, out_f32=res.out_f32,
-                      idx_out=res.idx, w_out=res.w, cnt_out=res.cnt, workspace=workspace, norm_pre=norm_pre,
-                      norm_post=norm_post, residual=residual, logits_out=res.logits)
+    d, ptr = dw.dims, B.ptr
+    p = B.MoeParams(T, top_k, D, d.num_experts, d.expert_dim, d.hidden_dim, ptr(x), ptr(dw.w_router), ptr(router_bias),
+                    ptr(dw.wg), ptr(dw.wu), ptr(dw.wd), ptr(dw.sg), ptr(dw.su), ptr(dw.sd), ptr(out), ptr(res.out_f32),
+                    ptr(res.idx), ptr(res.w), ptr(res.cnt), ptr(workspace),
+                    0 if workspace is None else workspace.numel(), ptr(norm_pre), ptr(norm_post), int(residual),
+                    ptr(res.logits))
     B.check(B.moe_block_forward_few(p, stream), "moe_block_forward_few")
     return res
 

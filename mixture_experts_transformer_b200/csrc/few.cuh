@@ -874,45 +874,56 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
       }
     }
   };
-  // The GeGLU row value of token t, column n of unit u (hidden unit f of N) from the parts of CTAs ca..cb, into the
-  // down chunks from chunk0 on. A warp's lanes hold 32 consecutive columns of one token.
-  auto finish_hidden = [&](const int* begin, int phase, int u, int ca, int cb, int t, int n, int f, int N, int chunk0) {
-    const float* src = P.part_gu + static_cast<size_t>(phase) * 2 * kUnit + t * kFewGuCols + n;
-    float gs = 0.f, us = 0.f;
-    for (int c0 = ca; c0 <= cb; c0 += 8) {
-      float a[8], b[8];
+  // GeGLU row values of tokens t0, t0 + step, ... (kTB of them, below T), column n of unit u (hidden unit f of N), from
+  // the parts of CTAs ca..cb in their order, into the down chunks from chunk0 on. A warp's lanes hold 32 consecutive
+  // columns. All loads of up to 4 CTAs' parts are in flight together.
+  constexpr int kTB = 4;
+  auto finish_hidden = [&](const int* begin, int phase, int u, int ca, int cb, int t0, int step, int n, int f, int N,
+                           int chunk0) {
+    const float* src = P.part_gu + static_cast<size_t>(phase) * 2 * kUnit + t0 * kFewGuCols + n;
+    float gs[kTB] = {}, us[kTB] = {};
+    for (int c0 = ca; c0 <= cb; c0 += 4) {
+      float a[4][kTB], b[4][kTB];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        a[c] = b[c] = 0.f;
-        if (c0 + c <= cb) {
-          const int sg = begin[c0 + c] >= u * ck ? 0 : 1;  // the unit is the first of its range
-          const float* at = src + (static_cast<size_t>(c0 + c) * 4 + sg) * kUnit;
-          a[c] = __ldcg(at);
-          b[c] = __ldcg(at + 16 * kFewGuCols);
+      for (int c = 0; c < 4; ++c) {
+        // seg 0: the unit is the first of the CTA's range
+        const float* at = src + (static_cast<size_t>(c0 + c) * 4 + (c0 + c <= cb && begin[c0 + c] < u * ck ? 1 : 0)) * kUnit;
+#pragma unroll
+        for (int j = 0; j < kTB; ++j) {
+          const bool in = c0 + c <= cb && t0 + j * step < P.T;
+          a[c][j] = in ? __ldcg(at + j * step * kFewGuCols) : 0.f;
+          b[c][j] = in ? __ldcg(at + (16 + j * step) * kFewGuCols) : 0.f;
         }
       }
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        gs += a[c];
-        us += b[c];
-      }
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int j = 0; j < kTB; ++j) {
+          gs[j] += a[c][j];
+          us[j] += b[c][j];
+        }
     }
-    const float h = gelu_tanh_exact(gs) * us;
-    if constexpr (MX) {
-      const uint32_t sc = mx_scale_code(__reduce_max_sync(0xffffffffu, abs_bits(h)));  // a group per warp
-      if (f < N) {
-        uint8_t* hc = P.h + static_cast<size_t>(chunk0 + (f >> 7)) * hchunk;
-        const float x = h * mx_inv_scale(sc);
-        hc[swz128(t, (f & 127) >> 4) + (f & 15)] = static_cast<uint8_t>(e4m3x4(x, x, x, x) & 0xFFu);
-        if (lane == 0) hc[16 * 128 + 16 * t + ((f & 127) >> 5)] = static_cast<uint8_t>(sc);
+#pragma unroll
+    for (int j = 0; j < kTB; ++j) {
+      const int t = t0 + j * step;
+      if (t >= P.T) break;
+      const float h = gelu_tanh_exact(gs[j]) * us[j];
+      if constexpr (MX) {
+        const uint32_t sc = mx_scale_code(__reduce_max_sync(0xffffffffu, abs_bits(h)));  // a group per warp
+        if (f < N) {
+          uint8_t* hc = P.h + static_cast<size_t>(chunk0 + (f >> 7)) * hchunk;
+          const float x = h * mx_inv_scale(sc);
+          hc[swz128(t, (f & 127) >> 4) + (f & 15)] = static_cast<uint8_t>(e4m3x4(x, x, x, x) & 0xFFu);
+          if (lane == 0) hc[16 * 128 + 16 * t + ((f & 127) >> 5)] = static_cast<uint8_t>(sc);
+        }
+      } else if (f < N) {
+        const __nv_bfloat16 hi = __float2bfloat16_rn(h);
+        // an infinity or NaN stays in the high part
+        const float lo = abs_bits(__bfloat162float(hi)) >= 0x7F800000u ? 0.f : h - __bfloat162float(hi);
+        uint8_t* at = P.h + static_cast<size_t>(chunk0 + (f >> 6)) * hchunk + swz128(t, (f & 63) >> 3) + (f & 7) * 2;
+        *reinterpret_cast<__nv_bfloat16*>(at) = hi;
+        *reinterpret_cast<__nv_bfloat16*>(at + rows * 128) = __float2bfloat16_rn(lo);
       }
-    } else if (f < N) {
-      const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-      // an infinity or NaN stays in the high part
-      const float lo = abs_bits(__bfloat162float(hi)) >= 0x7F800000u ? 0.f : h - __bfloat162float(hi);
-      uint8_t* at = P.h + static_cast<size_t>(chunk0 + (f >> 6)) * hchunk + swz128(t, (f & 63) >> 3) + (f & 7) * 2;
-      *reinterpret_cast<__nv_bfloat16*>(at) = hi;
-      *reinterpret_cast<__nv_bfloat16*>(at + rows * 128) = __float2bfloat16_rn(lo);
     }
   };
   for (int i = sBegS[cta]; i < sBegS[cta + 1];) {  // at most two units: there are no more units than CTAs
@@ -931,7 +942,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     const FewSplit split_s(su * ck, grid);
     for (int it = cta * 256 + ct; it < P.T * P.S; it += grid * 256) {
       const int t = it / P.S, f = it - t * P.S, u = f / kFewGuCols;
-      finish_hidden(sBegS, 0, u, split_s.cta_of(u * ck), split_s.cta_of((u + 1) * ck - 1), t, f % kFewGuCols, f, P.S, 0);
+      finish_hidden(sBegS, 0, u, split_s.cta_of(u * ck), split_s.cta_of((u + 1) * ck - 1), t, kFewMaxTokens,
+                    f % kFewGuCols, f, P.S, 0);
     }
     fence_proxy_async();
     const int e0 = sBegE[cta], e1 = sBegE[cta + 1];
@@ -950,10 +962,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
       bar_named(1, 32 * kFewConsWarps);
       if (*sLast) {
         const int e = u / fu, f0 = (u - e * fu) * kFewGuCols;
-        for (int it = ct; it < P.T * kFewGuCols; it += 256) {
-          const int n = it % kFewGuCols;
-          finish_hidden(sBegE, 1, u, ca, cb, it / kFewGuCols, n, f0 + n, P.F, ks_dn + e * ke_dn);
-        }
+        const int n = ct % kFewGuCols;
+        for (int t = ct / kFewGuCols; t < P.T; t += 2 * kTB)
+          finish_hidden(sBegE, 1, u, ca, cb, t, 2, n, f0 + n, P.F, ks_dn + e * ke_dn);
         fence_proxy_async();
       }
       bar_named(1, 32 * kFewConsWarps);  // sLast is free again
