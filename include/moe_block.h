@@ -585,7 +585,8 @@ moe_status moe_mxfp8_quantize_act(const void* x, int rows, int K, uint8_t* q, ui
  * the stream is being captured, where NULL returns MOE_ERR_WORKSPACE (the
  * cached allocation may be freed to grow while the graph still lives). At most
  * MOE_FEW_MAX_TOKENS tokens (with the other limits of moe_block_forward_few)
- * run in that form, more as grouped GEMMs.
+ * run in that form, more as grouped GEMMs. A workspace of T tokens serves
+ * every smaller batch too.
  */
 typedef struct moe_mxfp8_params {
   int T;

@@ -133,11 +133,21 @@ def ptr(t) -> int | None:
     return t.data_ptr()
 
 
-def stream_handle(stream=None) -> int | None:
-    import torch
+_raw_stream = None
 
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+
+def stream_handle(stream=None) -> int | None:
+    """The cudaStream_t of a torch stream (None: the current stream of the current device)."""
+    global _raw_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        import torch
+
+        torch.cuda.current_stream()  # (initialises CUDA)
+        _raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
+    device, raw = _raw_stream
+    return raw(device())
 
 
 def make_params(

@@ -304,19 +304,20 @@ def forward_wq(ww: WqWeights, x: torch.Tensor, *, top_k: int = B.TOP_K, router_b
 # ----------------------------------- few tokens, MXFP8 and the add-norm
 
 
-def _rows(name: str, t: torch.Tensor, shape, dtypes, device) -> torch.Tensor:
-    """t itself, after checking that it is a contiguous [shape] tensor of one of `dtypes` on `device`."""
-    if t.shape != shape or t.dtype not in dtypes or t.device != device or not t.is_contiguous():
+def _rows(name: str, t: torch.Tensor, shape, dtypes, device: int) -> int:
+    """t's address, after checking that it is a contiguous [shape] tensor of one of `dtypes` on CUDA device `device`."""
+    if t.shape != shape or t.dtype not in dtypes or t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"{name}: needs a contiguous {tuple(shape)} tensor of {' or '.join(map(str, dtypes))} on "
-                         f"{device}, got {tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
-    return t
+                         f"cuda:{device}, got {tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
+    return t.data_ptr()
 
 
-def _on_current_device(x: torch.Tensor) -> torch.device:
-    """x's device, which has to be the current one: the library launches there."""
-    if x.device.type != "cuda" or x.device.index != torch.cuda.current_device():
+def _on_current_device(x: torch.Tensor) -> int:
+    """The index of x's device, which has to be the current one: the library launches there."""
+    index = x.get_device()
+    if index < 0 or index != torch.cuda.current_device():
         raise ValueError(f"x is on {x.device}: the library runs on the current CUDA device")
-    return x.device
+    return index
 
 
 _BF16, _E4M3, _E8M0 = (torch.bfloat16,), (torch.float8_e4m3fn, torch.uint8), (torch.float8_e8m0fnu, torch.uint8)
@@ -353,10 +354,12 @@ def forward_few(
         _rows("router_bias", router_bias, (dw.dims.num_experts,), (torch.float32,), dev)
     if workspace is not None:
         _rows("workspace", workspace, workspace.shape, (torch.uint8,), dev)
-    out = torch.empty_like(x) if out is None else _rows("out", out, (T, D), _BF16, dev)
+    if out is None:
+        out = torch.empty_like(x)
+    _rows("out", out, (T, D), _BF16, dev)
     res = _result(out, dw.dims, top_k, debug)
     if debug:
-        res.logits = torch.empty((T, dw.dims.num_experts), dtype=torch.float32, device=dev)
+        res.logits = torch.empty((T, dw.dims.num_experts), dtype=torch.float32, device=x.device)
     d, ptr = dw.dims, B.ptr
     p = B.MoeParams(T, top_k, D, d.num_experts, d.expert_dim, d.hidden_dim, ptr(x), ptr(dw.w_router), ptr(router_bias),
                     ptr(dw.wg), ptr(dw.wu), ptr(dw.wd), ptr(dw.sg), ptr(dw.su), ptr(dw.sd), ptr(out), ptr(res.out_f32),
@@ -396,22 +399,26 @@ def add_rms_norm(
     e4m3 and scale [T, D/32] e8m0. Outputs may be passed in; y and sum_out may
     each be x or residual itself (in place)."""
     dev = _on_current_device(x)
-    T, D = x.shape
-    shape = (T, D)
-    _rows("x", x, shape, _BF16, dev)
-    for name, t, s in (("residual", residual, shape), ("gamma", gamma, (D,)), ("gamma_post", gamma_post, (D,)),
-                       ("y", y, shape), ("sum_out", sum_out, shape)):
-        if t is not None:
-            _rows(name, t, s, _BF16, dev)
-    y = torch.empty_like(x) if y is None else y
-    sum_out = torch.empty_like(x) if sum_out is None else sum_out
+    shape = x.shape
+    T, D = shape
+    px = _rows("x", x, shape, _BF16, dev)
+    pres = None if residual is None else _rows("residual", residual, shape, _BF16, dev)
+    pgam = None if gamma is None else _rows("gamma", gamma, (D,), _BF16, dev)
+    ppost = None if gamma_post is None else _rows("gamma_post", gamma_post, (D,), _BF16, dev)
+    if y is None:
+        y = torch.empty_like(x)
+    if sum_out is None:
+        sum_out = torch.empty_like(x)
+    py, psum = _rows("y", y, shape, _BF16, dev), _rows("sum_out", sum_out, shape, _BF16, dev)
+    pq = pscale = None
     if quantize or q is not None or scale is not None:
-        q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev) if q is None else _rows("q", q, shape, _E4M3, dev)
-        sshape = (T, D // B.MXFP8_GROUP)
-        scale = (torch.empty(sshape, dtype=torch.float8_e8m0fnu, device=dev) if scale is None
-                 else _rows("scale", scale, sshape, _E8M0, dev))
-    p = B.MoeNormParams(T, D, eps, x.data_ptr(), B.ptr(residual), B.ptr(gamma_post), B.ptr(gamma), sum_out.data_ptr(),
-                        y.data_ptr(), B.ptr(q), B.ptr(scale))
+        if q is None:
+            q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
+        if scale is None:
+            scale = torch.empty((T, D // B.MXFP8_GROUP), dtype=torch.float8_e8m0fnu, device=x.device)
+        pq = _rows("q", q, shape, _E4M3, dev)
+        pscale = _rows("scale", scale, (T, D // B.MXFP8_GROUP), _E8M0, dev)
+    p = B.MoeNormParams(T, D, eps, px, pres, ppost, pgam, psum, py, pq, pscale)
     B.check(B.moe_add_rms_norm(p, stream), "moe_add_rms_norm")
     return NormResult(y, sum_out, q, scale)
 
@@ -447,8 +454,8 @@ def quantize_mxfp8_rows(x: torch.Tensor, stream=None) -> tuple[torch.Tensor, tor
     T, D = x.shape
     dev = _on_current_device(x)
     _rows("x", x, (T, D), _BF16, dev)
-    q = torch.empty((T, D), dtype=torch.float8_e4m3fn, device=dev)
-    scale = torch.empty((T, D // B.MXFP8_GROUP), dtype=torch.float8_e8m0fnu, device=dev)
+    q = torch.empty((T, D), dtype=torch.float8_e4m3fn, device=x.device)
+    scale = torch.empty((T, D // B.MXFP8_GROUP), dtype=torch.float8_e8m0fnu, device=x.device)
     B.check(B.moe_mxfp8_quantize_act(x, T, D, q, scale, stream), "moe_mxfp8_quantize_act")
     return q, scale
 
@@ -514,7 +521,9 @@ def forward_mxfp8(
         _rows("router_bias", router_bias, (mw.dims.num_experts,), (torch.float32,), dev)
     if workspace is not None:
         _rows("workspace", workspace, workspace.shape, (torch.uint8,), dev)
-    out = torch.empty_like(x) if out is None else _rows("out", out, (T, D), _BF16, dev)
+    if out is None:
+        out = torch.empty_like(x)
+    _rows("out", out, (T, D), _BF16, dev)
     res = _result(out, mw.dims, top_k, debug)
     p = mxfp8_params(mw, T, x, out, xq=xq, xs=xs, top_k=top_k, router_bias=router_bias, res=res, workspace=workspace)
     B.check(B.moe_block_forward_mxfp8(p, stream), "moe_block_forward_mxfp8")

@@ -254,8 +254,8 @@ __device__ __forceinline__ uint32_t swz128(int t, int p) { return t * 128 + ((p 
 template <bool MX>
 __global__ void __launch_bounds__(kFewPrepThreads) few_prep_kernel(const __grid_constant__ FewParams P) {
   __shared__ float s_red[kFewPrepThreads / 32];
-  pdl_wait_then_release();
   const int t = blockIdx.x, tx = threadIdx.x;
+  pdl_wait_then_release();
   for (int i = t * kFewPrepThreads + tx; i < P.ncounters; i += gridDim.x * kFewPrepThreads) P.counters[i] = 0;
   const int nvec = P.D >> 3;  // 16-byte vectors of a bf16 row: at most two per thread
   constexpr int kV = kFewMaxDim / 8 / kFewPrepThreads;
@@ -409,10 +409,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     tmem_alloc(tmem_slot, kFewTmemCols);
     tmem_relinquish();
   }
+  // The kernel may start while few_prep_kernel runs: only the weight copies (threads 0 .. 3) go ahead of its end.
+  if (warp >= kFewProdWarps) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (threadIdx.x <= grid) sBegS[threadIdx.x] = FewSplit(su * ck, grid).begin(threadIdx.x);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  // The next kernel may be set up from now on (the library's wait for this one's end before they touch memory).
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
 
   if (warp < kFewProdWarps || warp == kFewProdWarp4) {
@@ -701,67 +705,91 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
       int got = 0;
       if (lane == 0) got = counter_wait(c_router, nr, abort_flag, P.err);
       got = __shfl_sync(0xffffffffu, got, 0);  // (a wait that gave up has raised abort)
-      for (int t = wr; t < P.T && got; t += 8) {
-        // this lane's experts 4 lane .. 4 lane + 3: the partial logits in CTA order
-        float l[4] = {0.f, 0.f, 0.f, 0.f};
+      if (got) {
+        // tokens wr and wr + 8 (if there) side by side; this lane's experts 4 lane .. 4 lane + 3
+        const int ntok = wr + 8 < P.T ? 2 : 1;
         const int e4 = lane * 4;
         const bool in = e4 < P.E;
-        const float4* part = reinterpret_cast<const float4*>(P.logit_part) + t * 32 + lane;
-        for (int r0 = 0; r0 < nr; r0 += 8) {
-          float4 v[8];
+        float l[2][4] = {};
+        for (int r0 = 0; r0 < nr; r0 += 4) {  // the partial logits in CTA order
+          float4 v[2][4];
 #pragma unroll
-          for (int r = 0; r < 8; ++r)
-            v[r] = r0 + r < nr ? __ldcg(part + (r0 + r) * 16 * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            l[0] += v[r].x;
-            l[1] += v[r].y;
-            l[2] += v[r].z;
-            l[3] += v[r].w;
+            for (int r = 0; r < 4; ++r)
+              v[h][r] = r0 + r < nr && h < ntok
+                            ? __ldcg(reinterpret_cast<const float4*>(P.logit_part) + ((r0 + r) * 16 + wr + 8 * h) * 32 + lane)
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              l[h][0] += v[h][r].x;
+              l[h][1] += v[h][r].y;
+              l[h][2] += v[h][r].z;
+              l[h][3] += v[h][r].w;
+            }
+        }
+        uint32_t key[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (in && P.bias) l[h][i] += __ldg(P.bias + e4 + i);
+            key[h][i] = in ? max(order_key(l[h][i] + 0.f), 1u) : 0u;  // (-0 + 0 = +0); key 0: not to be taken
+            if (in && h < ntok && cta == 0 && P.logits_out)
+              P.logits_out[static_cast<size_t>(wr + 8 * h) * P.E + e4 + i] = l[h][i];
           }
-        }
-        uint32_t key[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (in && P.bias) l[i] += __ldg(P.bias + e4 + i);
-          key[i] = in ? max(order_key(l[i] + 0.f), 1u) : 0u;  // (-0 + 0 = +0); key 0: not to be taken
-          if (in && cta == 0 && P.logits_out) P.logits_out[static_cast<size_t>(t) * P.E + e4 + i] = l[i];
-        }
         for (int j = 0; j < P.k; ++j) {
           // the largest key, the lowest expert among equals
-          uint32_t bk = key[0];
-          int be = e4;
+          uint32_t bk[2], top[2];
+          int be[2], e[2];
 #pragma unroll
-          for (int i = 1; i < 4; ++i)
-            if (key[i] > bk) {
-              bk = key[i];
-              be = e4 + i;
-            }
-          const uint32_t top = __reduce_max_sync(0xffffffffu, bk);
-          const int e = static_cast<int>(__reduce_min_sync(0xffffffffu, bk == top ? static_cast<uint32_t>(be) : 0xFFFFu));
-          if (e4 == (e & ~3)) {
+          for (int h = 0; h < 2; ++h) {
+            bk[h] = key[h][0];
+            be[h] = e4;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if ((e & 3) == i) {
-                sSel[t * kFewMaxTopK + j] = l[i];
-                key[i] = 0u;
+            for (int i = 1; i < 4; ++i)
+              if (key[h][i] > bk[h]) {
+                bk[h] = key[h][i];
+                be[h] = e4 + i;
               }
-            sCh[t * kFewMaxTopK + j] = static_cast<uint8_t>(e);
-            if (cta == 0 && P.idx_out) P.idx_out[static_cast<size_t>(t) * P.k + j] = e;
-            if (e >= P.e0 && e < P.e0 + P.el) atomicOr(&sTouched[e >> 5], 1u << (e & 31));
           }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) top[h] = __reduce_max_sync(0xffffffffu, bk[h]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            e[h] = static_cast<int>(
+                __reduce_min_sync(0xffffffffu, bk[h] == top[h] ? static_cast<uint32_t>(be[h]) : 0xFFFFu));
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (h < ntok && e4 == (e[h] & ~3)) {
+              const int t = wr + 8 * h;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if ((e[h] & 3) == i) {
+                  sSel[t * kFewMaxTopK + j] = l[h][i];
+                  key[h][i] = 0u;
+                }
+              sCh[t * kFewMaxTopK + j] = static_cast<uint8_t>(e[h]);
+              if (cta == 0 && P.idx_out) P.idx_out[static_cast<size_t>(t) * P.k + j] = e[h];
+              if (e[h] >= P.e0 && e[h] < P.e0 + P.el) atomicOr(&sTouched[e[h] >> 5], 1u << (e[h] & 31));
+            }
         }
         __syncwarp();
-        // softmax over the kept logits (slot 0 holds the largest), slot `lane`
-        const float top = sSel[t * kFewMaxTopK];
-        const float ex = lane < P.k ? expf(sSel[t * kFewMaxTopK + lane] - top) : 0.f;
-        float sum = ex;
+        for (int h = 0; h < ntok; ++h) {
+          // softmax over the kept logits (slot 0 holds the largest), slot `lane`
+          const int t = wr + 8 * h;
+          const float mx = sSel[t * kFewMaxTopK];
+          const float ex = lane < P.k ? expf(sSel[t * kFewMaxTopK + lane] - mx) : 0.f;
+          float sum = ex;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        __syncwarp();
-        if (lane < P.k) {
-          sSel[t * kFewMaxTopK + lane] = ex / sum;
-          if (cta == 0 && P.w_out) P.w_out[static_cast<size_t>(t) * P.k + lane] = ex / sum;
+          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          __syncwarp();
+          if (lane < P.k) {
+            sSel[t * kFewMaxTopK + lane] = ex / sum;
+            if (cta == 0 && P.w_out) P.w_out[static_cast<size_t>(t) * P.k + lane] = ex / sum;
+          }
         }
       }
     }
@@ -855,81 +883,63 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     publish(c_router);
   }
 
-  // ---- S, E: each run of a unit's chunks leaves its sums in part_gu. The shared MLP's GeGLU rows are made by all CTAs
-  // while the first experts' weights arrive; an expert unit's by its last CTA.
+  // ---- S, E: a unit's sums (this thread: column `col`, tokens 8 half ..) come from one CTA, or as parts from several,
+  // each part in its CTA's slot of part_gu. The shared MLP's GeGLU rows are made by all CTAs while the first experts'
+  // weights arrive; an expert unit's by the last of its CTAs.
   constexpr size_t kUnit = 2 * 16 * kFewGuCols;  // floats of a unit's partial sums
-  auto store_partial = [&](int phase, int seg) {
+  auto load_acc = [&](float (&g)[8], float (&v)[8]) {
     wait_acc();
-    uint32_t g[8], v[8];
-    tmem_ld_32x32b_x8(tlane + (q & 1) * kFewTmemAcc + half * 8, g);
-    tmem_ld_32x32b_x8(tlane + (q & 1) * kFewTmemAcc + 16 + half * 8, v);
+    uint32_t a[8], b[8];
+    tmem_ld_32x32b_x8(tlane + (q & 1) * kFewTmemAcc + half * 8, a);
+    tmem_ld_32x32b_x8(tlane + (q & 1) * kFewTmemAcc + 16 + half * 8, b);
     free_acc();
-    float* part = P.part_gu + ((static_cast<size_t>(cta) * 2 + phase) * 2 + seg) * kUnit;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      g[j] = __uint_as_float(a[j]);
+      v[j] = __uint_as_float(b[j]);
+    }
+  };
+  auto part_of = [&](int c, int phase, int seg) -> float* {  // gate sums [16][128], then up
+    return P.part_gu + ((static_cast<size_t>(c) * 2 + phase) * 2 + seg) * kUnit;
+  };
+  auto store_partial = [&](int phase, int seg, uint32_t tokens, const float (&g)[8], const float (&v)[8]) {
+    float* part = part_of(cta, phase, seg);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int t = half * 8 + j;
-      if (t < P.T) {
-        part[t * kFewGuCols + col] = __uint_as_float(g[j]);
-        part[(16 + t) * kFewGuCols + col] = __uint_as_float(v[j]);
+      if ((tokens >> t) & 1u) {
+        part[t * kFewGuCols + col] = g[j];
+        part[(16 + t) * kFewGuCols + col] = v[j];
       }
     }
   };
-  // GeGLU row values of tokens t0, t0 + step, ... (kTB of them, below T), column n of unit u (hidden unit f of N), from
-  // the parts of CTAs ca..cb in their order, into the down chunks from chunk0 on. A warp's lanes hold 32 consecutive
-  // columns. All loads of up to 4 CTAs' parts are in flight together.
-  constexpr int kTB = 4;
-  auto finish_hidden = [&](const int* begin, int phase, int u, int ca, int cb, int t0, int step, int n, int f, int N,
-                           int chunk0) {
-    const float* src = P.part_gu + static_cast<size_t>(phase) * 2 * kUnit + t0 * kFewGuCols + n;
-    float gs[kTB] = {}, us[kTB] = {};
-    for (int c0 = ca; c0 <= cb; c0 += 4) {
-      float a[4][kTB], b[4][kTB];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        // seg 0: the unit is the first of the CTA's range
-        const float* at = src + (static_cast<size_t>(c0 + c) * 4 + (c0 + c <= cb && begin[c0 + c] < u * ck ? 1 : 0)) * kUnit;
-#pragma unroll
-        for (int j = 0; j < kTB; ++j) {
-          const bool in = c0 + c <= cb && t0 + j * step < P.T;
-          a[c][j] = in ? __ldcg(at + j * step * kFewGuCols) : 0.f;
-          b[c][j] = in ? __ldcg(at + (16 + j * step) * kFewGuCols) : 0.f;
-        }
+  // One GeGLU value (token t, hidden unit f of N) into the down chunks from chunk0 on. A warp's lanes hold 32
+  // consecutive f, an MXFP8 group.
+  auto emit_hidden = [&](int t, int f, int N, int chunk0, float gate, float up) {
+    const float h = gelu_tanh_exact(gate) * up;
+    if constexpr (MX) {
+      const uint32_t sc = mx_scale_code(__reduce_max_sync(0xffffffffu, abs_bits(h)));
+      if (f < N) {
+        uint8_t* hc = P.h + static_cast<size_t>(chunk0 + (f >> 7)) * hchunk;
+        const float x = h * mx_inv_scale(sc);
+        hc[swz128(t, (f & 127) >> 4) + (f & 15)] = static_cast<uint8_t>(e4m3x4(x, x, x, x) & 0xFFu);
+        if (lane == 0) hc[16 * 128 + 16 * t + ((f & 127) >> 5)] = static_cast<uint8_t>(sc);
       }
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int j = 0; j < kTB; ++j) {
-          gs[j] += a[c][j];
-          us[j] += b[c][j];
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < kTB; ++j) {
-      const int t = t0 + j * step;
-      if (t >= P.T) break;
-      const float h = gelu_tanh_exact(gs[j]) * us[j];
-      if constexpr (MX) {
-        const uint32_t sc = mx_scale_code(__reduce_max_sync(0xffffffffu, abs_bits(h)));  // a group per warp
-        if (f < N) {
-          uint8_t* hc = P.h + static_cast<size_t>(chunk0 + (f >> 7)) * hchunk;
-          const float x = h * mx_inv_scale(sc);
-          hc[swz128(t, (f & 127) >> 4) + (f & 15)] = static_cast<uint8_t>(e4m3x4(x, x, x, x) & 0xFFu);
-          if (lane == 0) hc[16 * 128 + 16 * t + ((f & 127) >> 5)] = static_cast<uint8_t>(sc);
-        }
-      } else if (f < N) {
-        const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-        // an infinity or NaN stays in the high part
-        const float lo = abs_bits(__bfloat162float(hi)) >= 0x7F800000u ? 0.f : h - __bfloat162float(hi);
-        uint8_t* at = P.h + static_cast<size_t>(chunk0 + (f >> 6)) * hchunk + swz128(t, (f & 63) >> 3) + (f & 7) * 2;
-        *reinterpret_cast<__nv_bfloat16*>(at) = hi;
-        *reinterpret_cast<__nv_bfloat16*>(at + rows * 128) = __float2bfloat16_rn(lo);
-      }
+    } else if (f < N) {
+      const __nv_bfloat16 hi = __float2bfloat16_rn(h);
+      // an infinity or NaN stays in the high part
+      const float lo = abs_bits(__bfloat162float(hi)) >= 0x7F800000u ? 0.f : h - __bfloat162float(hi);
+      uint8_t* at = P.h + static_cast<size_t>(chunk0 + (f >> 6)) * hchunk + swz128(t, (f & 63) >> 3) + (f & 7) * 2;
+      *reinterpret_cast<__nv_bfloat16*>(at) = hi;
+      *reinterpret_cast<__nv_bfloat16*>(at + rows * 128) = __float2bfloat16_rn(lo);
     }
   };
   for (int i = sBegS[cta]; i < sBegS[cta + 1];) {  // at most two units: there are no more units than CTAs
     const int u = i / ck;
     i = min(sBegS[cta + 1], (u + 1) * ck);
-    store_partial(0, u == sBegS[cta] / ck ? 0 : 1);
+    float g[8], v[8];
+    load_acc(g, v);
+    store_partial(0, u == sBegS[cta] / ck ? 0 : 1, (1u << P.T) - 1u, g, v);
   }
   publish(c_shared);
   if (ct == 0)
@@ -942,29 +952,89 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     const FewSplit split_s(su * ck, grid);
     for (int it = cta * 256 + ct; it < P.T * P.S; it += grid * 256) {
       const int t = it / P.S, f = it - t * P.S, u = f / kFewGuCols;
-      finish_hidden(sBegS, 0, u, split_s.cta_of(u * ck), split_s.cta_of((u + 1) * ck - 1), t, kFewMaxTokens,
-                    f % kFewGuCols, f, P.S, 0);
+      const int ca = split_s.cta_of(u * ck), cb = split_s.cta_of((u + 1) * ck - 1);
+      float gs = 0.f, us = 0.f;
+      for (int c0 = ca; c0 <= cb; c0 += 8) {
+        float a[8], b[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          a[c] = b[c] = 0.f;
+          if (c0 + c <= cb) {  // slot 0: the unit is the first of the CTA's range
+            const float* at = part_of(c0 + c, 0, sBegS[c0 + c] >= u * ck ? 0 : 1) + t * kFewGuCols + f % kFewGuCols;
+            a[c] = __ldcg(at);
+            b[c] = __ldcg(at + 16 * kFewGuCols);
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          gs += a[c];
+          us += b[c];
+        }
+      }
+      emit_hidden(t, f, P.S, 0, gs, us);
     }
     fence_proxy_async();
     const int e0 = sBegE[cta], e1 = sBegE[cta + 1];
     for (int i = e0; i < e1;) {
       const int u = i / ck;
-      const int seg = u == e0 / ck ? 0 : 1;
-      // middle units (neither first nor last of the range) are whole and use the last unit's slot in turn
+      const int seg = u == e0 / ck ? 0 : 1;  // (middle units of a range are whole and leave no part)
       i = min(e1, (u + 1) * ck);
-      store_partial(1, seg);
+      float g[8], v[8];
+      load_acc(g, v);
       // the CTAs that share the unit: this one's neighbours
       int ca = cta, cb = cta;
       while (sBegE[ca] > u * ck) --ca;
       while (sBegE[cb + 1] < (u + 1) * ck) ++cb;
-      const uint32_t before = publish(c_eu + u);
-      if (ct == 0) *sLast = ok && before == static_cast<uint32_t>(cb - ca) ? 1 : 0;
-      bar_named(1, 32 * kFewConsWarps);
+      const uint32_t tokens = sBits[u / fu];  // only the tokens routed to the expert are kept
+      bool own = true;                        // this CTA's part is still in registers
+      if (ca != cb) {
+        // When all others have left their parts, this one's need not go through memory.
+        const uint32_t others = static_cast<uint32_t>(cb - ca);
+        if (ct == 0) *sLast = ok && ld_acquire(c_eu + u) == others ? 1 : 0;
+        bar_named(1, 32 * kFewConsWarps);
+        if (*sLast == 0) {
+          bar_named(1, 32 * kFewConsWarps);
+          own = false;
+          store_partial(1, seg, tokens, g, v);
+          const uint32_t before = publish(c_eu + u);
+          if (ct == 0) *sLast = ok && before == others ? 1 : 0;
+          bar_named(1, 32 * kFewConsWarps);
+        }
+      } else {
+        if (ct == 0) *sLast = ok ? 1 : 0;
+        bar_named(1, 32 * kFewConsWarps);
+      }
       if (*sLast) {
-        const int e = u / fu, f0 = (u - e * fu) * kFewGuCols;
-        const int n = ct % kFewGuCols;
-        for (int t = ct / kFewGuCols; t < P.T; t += 2 * kTB)
-          finish_hidden(sBegE, 1, u, ca, cb, t, 2, n, f0 + n, P.F, ks_dn + e * ke_dn);
+        const int e = u / fu, f = (u - e * fu) * kFewGuCols + col;
+#pragma unroll
+        for (int j0 = 0; j0 < 8; j0 += 4) {
+          if (((tokens >> (half * 8 + j0)) & 15u) == 0) continue;
+          float gs[4] = {}, us[4] = {};
+          for (int c0 = ca; c0 <= cb; c0 += 2) {
+            float a[2][4], b[2][4];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const bool mine = own && c0 + c == cta, in = c0 + c <= cb && !mine;
+              const float* at = part_of(c0 + c, 1, in && sBegE[c0 + c] < u * ck ? 1 : 0) + (half * 8 + j0) * kFewGuCols + col;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const bool get = in && ((tokens >> (half * 8 + j0 + j)) & 1u);
+                a[c][j] = get ? __ldcg(at + j * kFewGuCols) : mine ? g[j0 + j] : 0.f;
+                b[c][j] = get ? __ldcg(at + (16 + j) * kFewGuCols) : mine ? v[j0 + j] : 0.f;
+              }
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                gs[j] += a[c][j];
+                us[j] += b[c][j];
+              }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if ((tokens >> (half * 8 + j0 + j)) & 1u) emit_hidden(half * 8 + j0 + j, f, P.F, ks_dn + e * ke_dn, gs[j], us[j]);
+        }
         fence_proxy_async();
       }
       bar_named(1, 32 * kFewConsWarps);  // sLast is free again

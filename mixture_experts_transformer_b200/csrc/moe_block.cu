@@ -1139,11 +1139,13 @@ cudaError_t launch_few(FewParams* P, int sm_count, cudaStream_t st) {
   cfg.blockDim = dim3(kFewThreads);
   cfg.dynamicSmemBytes = kFewFixedBytes + P->stages * few_stage_bytes<MX>(rows);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;  // the CTAs wait on one another: all must be resident
   attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, few_kernel<MX>, *P);
 }
 
@@ -1215,6 +1217,14 @@ moe_status enqueue_few_bf16(const moe_params* p, const Dims& d, const FewLayout&
     MOE_TRY(ls_.done(launch_k(guard_check_kernel, 1, kGuardWords, 0, st, static_cast<const uint32_t*>(guard), s->err)));
   }
   return MOE_OK;
+}
+
+// The workspace of an MXFP8 call: large enough for every smaller batch too, whichever form it takes.
+size_t mx_workspace_bytes(const Dims& d) {
+  Dims few = d;
+  few.T = std::min(d.T, kFewMaxTokens);
+  const size_t small = few_fits(few) ? make_few_layout(few, true).total : make_mx_layout(few).total;
+  return few_fits(d) ? small : std::max(small, make_mx_layout(d).total);
 }
 
 moe_status enqueue_few_mx(const moe_mxfp8_params* p, const Dims& d, const FewLayout& L, uint8_t* ws, DeviceState* s,
@@ -2197,7 +2207,7 @@ size_t moe_mxfp8_workspace_bytes(const moe_mxfp8_params* p) {
   if (!p) return 0;
   const Dims d = mx_dims_of(p);
   if (!dims_ok(d)) return 0;
-  return few_fits(d) ? make_few_layout(d, true).total : make_mx_layout(d).total;
+  return mx_workspace_bytes(d);
 }
 
 moe_status moe_block_forward_mxfp8(const moe_mxfp8_params* p, void* stream) {

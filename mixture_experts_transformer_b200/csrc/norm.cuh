@@ -107,6 +107,48 @@ struct AddNormParams {
   uint8_t* scale;
 };
 
+// Two fp32 values in a 64-bit register pair, handled by the packed fp32
+// instructions: with one instruction per value the kernel spent 62% of its
+// issue slots and 78 us on 16384 rows of 2816 (every output), at 4.7 TB/s.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 bf16x2_to_f32x2(uint32_t u) {
+  return pack2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t f32x2_to_bf16x2(f32x2 v) {
+  float lo, hi;
+  unpack2(v, lo, hi);
+  return pack_bf16x2(lo, hi);
+}
+// the larger magnitude; a NaN stays one
+__device__ __forceinline__ float max_abs(float m, float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+  return r;
+}
+
 template <int TPR, int NV>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rms_norm_kernel(const AddNormParams P) {
   constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
@@ -122,45 +164,53 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rms_norm_kernel(con
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
     const int v = lane + u * TPR;
-    xv[u] = v < nvec ? reinterpret_cast<const uint4*>(P.x + row)[v] : make_uint4(0, 0, 0, 0);
+    xv[u] = rv[u] = make_uint4(0, 0, 0, 0);
+    if (v < nvec) xv[u] = reinterpret_cast<const uint4*>(P.x + row)[v];
   }
   if (P.residual) {
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       const int v = lane + u * TPR;
-      rv[u] = v < nvec ? reinterpret_cast<const uint4*>(P.residual + row)[v] : make_uint4(0, 0, 0, 0);
+      if (v < nvec) rv[u] = reinterpret_cast<const uint4*>(P.residual + row)[v];
     }
   }
-  float s[NV][8];
+  f32x2 s[NV][4];
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
-    const __nv_bfloat16* xb = reinterpret_cast<const __nv_bfloat16*>(&xv[u]);
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&xv[u]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[u][i] = __bfloat162float(xb[i]);
+    for (int i = 0; i < 4; ++i) s[u][i] = bf16x2_to_f32x2(w[i]);
   }
-  if (P.gamma_post) {
-    float ss = 0.f;
+  // 1 / rms of the row in s (elements past D are zero)
+  auto inv_rms = [&](float* red) -> float {
+    f32x2 ss = pack2(0.f, 0.f);
 #pragma unroll
     for (int u = 0; u < NV; ++u)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(s[u][i], s[u][i], ss);
-    const float r = 1.0f / sqrtf(row_sum<TPR>(ss, s_red[0]) * inv_d + P.eps);
+      for (int i = 0; i < 4; ++i) ss = fma2(s[u][i], s[u][i], ss);
+    float lo, hi;
+    unpack2(ss, lo, hi);
+    return 1.0f / sqrtf(row_sum<TPR>(lo + hi, red) * inv_d + P.eps);
+  };
+  if (P.gamma_post) {
+    const float r1 = inv_rms(s_red[0]);
+    const f32x2 r = pack2(r1, r1);
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       const int v = lane + u * TPR;
-      const uint4 gv =
-          v < nvec ? __ldg(reinterpret_cast<const uint4*>(P.gamma_post) + v) : make_uint4(0, 0, 0, 0);
-      const __nv_bfloat16* gb = reinterpret_cast<const __nv_bfloat16*>(&gv);
+      if (v >= nvec) continue;  // (stays zero)
+      const uint4 gv = __ldg(reinterpret_cast<const uint4*>(P.gamma_post) + v);
+      const uint32_t* g = reinterpret_cast<const uint32_t*>(&gv);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[u][i] = v < nvec ? s[u][i] * r * __bfloat162float(gb[i]) : 0.f;
+      for (int i = 0; i < 4; ++i) s[u][i] = mul2(mul2(s[u][i], r), bf16x2_to_f32x2(g[i]));
     }
   }
   if (P.residual) {
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
-      const __nv_bfloat16* rb = reinterpret_cast<const __nv_bfloat16*>(&rv[u]);
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&rv[u]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[u][i] += __bfloat162float(rb[i]);
+      for (int i = 0; i < 4; ++i) s[u][i] = add2(s[u][i], bf16x2_to_f32x2(w[i]));
     }
   }
   if (P.sum) {
@@ -168,47 +218,47 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rms_norm_kernel(con
     for (int u = 0; u < NV; ++u) {
       const int v = lane + u * TPR;
       if (v < nvec)
-        reinterpret_cast<uint4*>(P.sum + row)[v] =
-            make_uint4(pack_bf16x2(s[u][0], s[u][1]), pack_bf16x2(s[u][2], s[u][3]), pack_bf16x2(s[u][4], s[u][5]),
-                       pack_bf16x2(s[u][6], s[u][7]));
+        reinterpret_cast<uint4*>(P.sum + row)[v] = make_uint4(f32x2_to_bf16x2(s[u][0]), f32x2_to_bf16x2(s[u][1]),
+                                                              f32x2_to_bf16x2(s[u][2]), f32x2_to_bf16x2(s[u][3]));
     }
   }
   if (!P.y && !P.q) return;
-  float ss = 0.f;
-#pragma unroll
-  for (int u = 0; u < NV; ++u)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(s[u][i], s[u][i], ss);
-  const float r = 1.0f / sqrtf(row_sum<TPR>(ss, s_red[1]) * inv_d + P.eps);
+  const float r1 = inv_rms(s_red[1]);
+  const f32x2 r = pack2(r1, r1);
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
     const int v = lane + u * TPR;
     const bool in = v < nvec;
-    float o[8];
+    f32x2 o[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = s[u][i] * r;
-    if (P.gamma) {
-      const uint4 gv = in ? __ldg(reinterpret_cast<const uint4*>(P.gamma) + v) : make_uint4(0, 0, 0, 0);
-      const __nv_bfloat16* gb = reinterpret_cast<const __nv_bfloat16*>(&gv);
+    for (int i = 0; i < 4; ++i) o[i] = mul2(s[u][i], r);
+    if (P.gamma && in) {
+      const uint4 gv = __ldg(reinterpret_cast<const uint4*>(P.gamma) + v);
+      const uint32_t* g = reinterpret_cast<const uint32_t*>(&gv);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] *= __bfloat162float(gb[i]);
+      for (int i = 0; i < 4; ++i) o[i] = mul2(o[i], bf16x2_to_f32x2(g[i]));
     }
     if (P.y && in)
-      reinterpret_cast<uint4*>(P.y + row)[v] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
-                                                          pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+      reinterpret_cast<uint4*>(P.y + row)[v] = make_uint4(f32x2_to_bf16x2(o[0]), f32x2_to_bf16x2(o[1]),
+                                                          f32x2_to_bf16x2(o[2]), f32x2_to_bf16x2(o[3]));
     if (P.q) {
-      uint32_t m = 0;
+      float f[8], mf = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, abs_bits(o[i]));
+      for (int i = 0; i < 4; ++i) {
+        unpack2(o[i], f[2 * i], f[2 * i + 1]);
+        mf = max_abs(max_abs(mf, f[2 * i]), f[2 * i + 1]);
+      }
       // the four lanes of a 32-group (D is a multiple of 32: all in range, or none)
+      uint32_t m = __float_as_uint(mf) & 0x7FFFFFFFu;
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
       const uint32_t sc = mx_scale_code(m);
-      const float inv = mx_inv_scale(sc);
+      const float i1 = mx_inv_scale(sc);
+      const f32x2 inv = pack2(i1, i1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) unpack2(mul2(o[i], inv), f[2 * i], f[2 * i + 1]);
       if (in) {
-        reinterpret_cast<uint2*>(P.q + row)[v] =
-            make_uint2(e4m3x4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv),
-                       e4m3x4(o[4] * inv, o[5] * inv, o[6] * inv, o[7] * inv));
+        reinterpret_cast<uint2*>(P.q + row)[v] = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
         if ((v & 3) == 0) P.scale[static_cast<size_t>(t) * (P.D >> 5) + (v >> 2)] = static_cast<uint8_t>(sc);
       }
     }
