@@ -1,7 +1,7 @@
-// The whole MoE layer for a few tokens (T <= 16) in two kernels: a small one that
-// lays x out (norm_pre, or MXFP8 quantisation), and one cooperative kernel for
-// router, top-k, experts, shared MLP, combine and (bf16 form) norm_post and
-// residual.
+// The whole MoE layer for a few tokens (T <= 16) in two kernels: a small one for
+// the router's logits and x as MMA operands (norm_pre, or MXFP8 quantisation),
+// and one cooperative kernel for top-k, experts, shared MLP, combine and (bf16
+// form) norm_post and residual.
 //
 // A few tokens read every touched expert's weights once and compute almost
 // nothing per byte, so the layer is bound by HBM: the kernel is built as one
@@ -14,16 +14,17 @@
 //     falls inside an output column's reduction; CTAs that share a column
 //     leave fp32 partial sums, and the last of them adds them up in CTA order;
 //   * producer threads keep a ring of TMA copies full across the phases: the
-//     shared MLP's chunks need no routing, so they stream while the router's
-//     result is reduced, and the first down chunks are already in flight while
-//     the last GeGLU rows are being finished elsewhere.
+//     shared MLP's chunks need no routing, so they stream while the small kernel
+//     runs and the experts are chosen, and the first down chunks are already in
+//     flight while the last GeGLU rows are being finished elsewhere.
 //
-// Phases (chunk lists): R the router (the first CTAs, 256 K rows each),
-// S the shared MLP's gate|up, E the touched experts' gate|up, D all down
-// projections: for each 256 output columns the shared MLP's reduction, then
-// each touched expert's. Two grid-wide waits: the top-k needs all partial
-// logits, D needs all GeGLU rows. The grid is launched cooperatively (all CTAs
-// resident), and every wait is bounded.
+// Phases (chunk lists): S the shared MLP's gate|up, E the touched experts'
+// gate|up, D all down projections: for each 256 output columns the shared MLP's
+// reduction, then each touched expert's. Grid-wide waits: D needs all GeGLU rows,
+// the output all parts of D. The grid is launched cooperatively (all CTAs
+// resident), and every wait is bounded. The router as a phase of this kernel put
+// two more such hand-overs before the first expert chunk (routing known 11.9 us
+// after the start at T = 1).
 //
 // Products: tcgen05.mma with the weight columns as M = 128 and the tokens as
 // N = 16, one thread issuing 8 or 16 MMAs per chunk, so the SM's issue slots play no
@@ -49,7 +50,7 @@ namespace moe {
 constexpr int kFewMaxTokens = 16;
 constexpr int kFewMaxTopK = 32;
 constexpr int kFewMaxDim = 4096;  // at most 16 CTAs share the router's reduction
-constexpr int kFewPrepThreads = 256;
+constexpr int kFewPrepThreads = 512;
 constexpr int kFewConsWarps = 8;
 constexpr int kFewProdWarps = 4;  // copying threads 0..3, one a warp (the TMEM lane quarter of warp w is w % 4)
 constexpr int kFewMmaWarp = kFewProdWarps + 2 * kFewConsWarps;  // after 8 consumer and 8 routing warps
@@ -57,7 +58,7 @@ constexpr int kFewProdWarp4 = kFewMmaWarp + 1;                  // copying threa
 constexpr int kFewThreads = 32 * (kFewMmaWarp + 2);
 constexpr int kFewWBytes = 32768;    // weights of a chunk
 constexpr int kFewSfBytes = 1024;    // MXFP8: two scale tiles of a chunk
-constexpr int kFewRouterRows = 256;  // K rows of the router per CTA (4 chunks of 64)
+constexpr int kFewRouterRows = 256;  // K rows of the router per CTA of the small kernel
 constexpr int kFewGuCols = 128;      // output columns of a gate|up chunk, per projection
 constexpr int kFewDnCols = 256;      // output columns of a down chunk
 constexpr int kFewMaxStages = 8;
@@ -99,7 +100,6 @@ constexpr int kFewFixedBytes = 128 * 16 * 4 + 128 * 4 + 128            // weight
                                + 512 /* barriers, flags */ + 1024 /* alignment */;
 
 struct FewParams {
-  CUtensorMap tmR;  // w_router [D][E] bf16, box 64 columns x 64 K
   // experts (tmS*: shared). bf16 [el][K][N] in 64-column blocks of 64 K: G, U two adjacent blocks per copy, D four.
   // MXFP8 [el][N][K]: G, U 128 B x 128 rows, D 128 B x 256 rows. 128-byte swizzle.
   CUtensorMap tmG, tmU, tmD;
@@ -117,11 +117,11 @@ struct FewParams {
   const uint8_t* xs;
   const __nv_bfloat16* norm_pre;
   uint8_t* xb;  // x as B operands, one few_xchunk per K chunk
-  uint8_t* xr;  // x as the router's B operand: bf16, 64 K per block (bf16 form: xb)
+  const __nv_bfloat16* w_router;
   const __nv_bfloat16* norm_post;
   int residual;
   const float* bias;
-  uint32_t* counters;  // cleared by few_prep_kernel: router, hidden, down, shared, rows, then (8) one per E unit
+  uint32_t* counters;  // cleared by few_prep_kernel: hidden, down, shared, rows, then (8) one per E unit
   int ncounters;
   float* logit_part;   // [ceil(D / 256)][16][128]
   uint8_t* h;          // GeGLU rows, one few_hchunk per K chunk of down
@@ -198,14 +198,6 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
       : "r"(taddr)
       : "memory");
 }
-// A 512-byte scale tile from shared memory into 4 TMEM columns of every lane quarter (row i of 16 bytes to lane i).
-// In order with this thread's MMAs. Descriptor: no swizzle, 8-row groups 128 bytes apart.
-__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t saddr) {
-  asm volatile(
-      "{\n\t.reg .b64 a;\n\tmov.b64 a, {%1, %2};\n\ttcgen05.cp.cta_group::1.32x128b.warpx4 [%0], a;\n\t}" ::"r"(taddr),
-      "r"(saddr >> 4), "r"((128u >> 4) | (1u << 14))
-      : "memory");
-}
 // kind::f16, bf16, M = 128, A with its M index contiguous (bit 15), B K-major.
 __host__ __device__ constexpr uint32_t few_idesc_bf16(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (static_cast<uint32_t>(n >> 3) << 17) |
@@ -249,94 +241,149 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 // Byte of (token row t, 16-byte piece p) in a block of 128-byte rows with the 128-byte swizzle.
 __device__ __forceinline__ uint32_t swz128(int t, int p) { return t * 128 + ((p ^ (t & 7)) << 4); }
 
-// x as B operands, and the counters cleared: one CTA per token. Rows past T are left as they are: a token is a
-// column of every product, and columns past T are never read.
+// The small kernel. CTA c: partial logits of all tokens over K rows 256 c .. (fp32 multiply-adds of bf16 values, a
+// thread four experts over 16 rows, the 16 row groups added in order), token c as B operands, a share of the counters
+// cleared. Rows past T of the operands are left as they are: a token is a column of every product, and columns past T
+// are never read.
 template <bool MX>
 __global__ void __launch_bounds__(kFewPrepThreads) few_prep_kernel(const __grid_constant__ FewParams P) {
-  __shared__ float s_red[kFewPrepThreads / 32];
-  const int t = blockIdx.x, tx = threadIdx.x;
+  constexpr int kWarps = kFewPrepThreads / 32;
+  constexpr int kRowsPer = kFewRouterRows / kWarps;  // K rows of a warp
+  constexpr int kTB = 4;                             // tokens per pass
+  __shared__ __align__(16) __nv_bfloat16 s_x[kFewMaxTokens][kFewRouterRows];
+  __shared__ float4 s_part[kWarps][kTB][32];
+  __shared__ float s_rms[kFewMaxTokens];
+  const int c = blockIdx.x, tx = threadIdx.x, lane = tx & 31, warp = tx >> 5;
+  // the slice's weights into L2 while the previous kernel ends (a prefetch reads no value: it may come early)
+  if (tx < kFewRouterRows && c * kFewRouterRows + tx < P.D)
+    for (int o = 0; o < P.E; o += 64)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(P.w_router + static_cast<size_t>(c * kFewRouterRows + tx) * P.E + o));
   pdl_wait_then_release();
-  for (int i = t * kFewPrepThreads + tx; i < P.ncounters; i += gridDim.x * kFewPrepThreads) P.counters[i] = 0;
-  const int nvec = P.D >> 3;  // 16-byte vectors of a bf16 row: at most two per thread
-  constexpr int kV = kFewMaxDim / 8 / kFewPrepThreads;
-  const int rows = few_rows<MX>(P.T);
-  uint4 xv[kV];
+  for (int i = c * kFewPrepThreads + tx; i < P.ncounters; i += gridDim.x * kFewPrepThreads) P.counters[i] = 0;
+  const int D = P.D, nvec = D >> 3;  // 16-byte vectors of a bf16 row
+  const uint4* xrow = reinterpret_cast<const uint4*>(P.x);
+  const int k0 = c * kFewRouterRows;
+  const bool route = k0 < D, lay = c < P.T;
+  // the router's weights of this thread: experts 4 lane .., its warp's 16 rows
+  uint2 w[kRowsPer];
+  const bool in = route && lane * 4 < P.E;
 #pragma unroll
-  for (int u = 0; u < kV; ++u) {
-    const int v = tx + u * kFewPrepThreads;
-    xv[u] = v < nvec ? __ldg(reinterpret_cast<const uint4*>(P.x) + static_cast<size_t>(t) * nvec + v)
-                     : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < kRowsPer; ++i) {
+    const int k = k0 + warp * kRowsPer + i;
+    w[i] = in && k < D ? __ldg(reinterpret_cast<const uint2*>(P.w_router + static_cast<size_t>(k) * P.E) + lane)
+                       : make_uint2(0, 0);
   }
   if constexpr (!MX) {
-    if (P.norm_pre) {  // the same order of operations as rms_norm_rows_kernel's definition: bf16(x r gamma)
-      float ss = 0.f;
+    if (P.norm_pre) {  // 1 / rms of every row, a warp each
+      if (warp < P.T) {
+        float ss = 0.f;
+#pragma unroll 4
+        for (int v = lane; v < nvec; v += 32) {
+          const uint4 q = __ldg(xrow + static_cast<size_t>(warp) * nvec + v);
+          const __nv_bfloat16* b = reinterpret_cast<const __nv_bfloat16*>(&q);
 #pragma unroll
-      for (int u = 0; u < kV; ++u) {
-        const __nv_bfloat16* xb = reinterpret_cast<const __nv_bfloat16*>(&xv[u]);
+          for (int i = 0; i < 8; ++i) ss = fmaf(__bfloat162float(b[i]), __bfloat162float(b[i]), ss);
+        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(__bfloat162float(xb[i]), __bfloat162float(xb[i]), ss);
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (lane == 0) s_rms[warp] = 1.0f / sqrtf(ss / static_cast<float>(D) + 1e-6f);
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if ((tx & 31) == 0) s_red[tx >> 5] = ss;
       __syncthreads();
-      float tot = 0.f;
-#pragma unroll
-      for (int i = 0; i < kFewPrepThreads / 32; ++i) tot += s_red[i];
-      const float r = 1.0f / sqrtf(tot / static_cast<float>(P.D) + 1e-6f);
-#pragma unroll
-      for (int u = 0; u < kV; ++u) {
-        const int v = tx + u * kFewPrepThreads;
-        const uint4 gv = v < nvec ? __ldg(reinterpret_cast<const uint4*>(P.norm_pre) + v) : make_uint4(0, 0, 0, 0);
-        const __nv_bfloat16* xb = reinterpret_cast<const __nv_bfloat16*>(&xv[u]);
-        const __nv_bfloat16* gb = reinterpret_cast<const __nv_bfloat16*>(&gv);
-        float o[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = __bfloat162float(xb[j]) * r * __bfloat162float(gb[j]);
-        xv[u] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
-                           pack_bf16x2(o[6], o[7]));
-      }
     }
   }
+  // eight values of row t, after norm_pre (rounded to bf16: the layer's input)
+  auto load_x = [&](int t, int v) -> uint4 {
+    uint4 q = __ldg(xrow + static_cast<size_t>(t) * nvec + v);
+    if (!MX && P.norm_pre) {
+      const uint4 gv = __ldg(reinterpret_cast<const uint4*>(P.norm_pre) + v);
+      const __nv_bfloat16* b = reinterpret_cast<const __nv_bfloat16*>(&q);
+      const __nv_bfloat16* g = reinterpret_cast<const __nv_bfloat16*>(&gv);
+      const float r = s_rms[t];
+      float o[8];
 #pragma unroll
-  for (int u = 0; u < kV; ++u) {
-    const int v = tx + u * kFewPrepThreads;
-    if (v < nvec) *reinterpret_cast<uint4*>(P.xr + (v >> 3) * rows * 128 + swz128(t, v & 7)) = xv[u];
-  }
-  if constexpr (MX) {
-    const int xchunk = few_xchunk<true>(16);
-    if (P.xq) {
-      const int ng = P.D / kMxGroup;
-      for (int v = tx; v < (P.D >> 4); v += kFewPrepThreads)
-        *reinterpret_cast<uint4*>(P.xb + (v >> 3) * xchunk + swz128(t, v & 7)) =
-            __ldg(reinterpret_cast<const uint4*>(P.xq) + static_cast<size_t>(t) * (P.D >> 4) + v);
-      for (int g = tx; g < ng; g += kFewPrepThreads)
-        P.xb[(g >> 2) * xchunk + 16 * 128 + 16 * t + (g & 3)] = __ldg(P.xs + static_cast<size_t>(t) * ng + g);
+      for (int j = 0; j < 8; ++j) o[j] = __bfloat162float(b[j]) * r * __bfloat162float(g[j]);
+      q = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+    }
+    return q;
+  };
+  if (lay) {  // token c: at most one vector per thread
+    static_assert(kFewMaxDim / 8 <= kFewPrepThreads, "a row fits the block");
+    const int v = tx;
+    if constexpr (!MX) {
+      const int rows = few_rows<MX>(P.T);
+      if (v < nvec) *reinterpret_cast<uint4*>(P.xb + (v >> 3) * rows * 128 + swz128(c, v & 7)) = load_x(c, v);
     } else {
-#pragma unroll
-      for (int u = 0; u < kV; ++u) {  // four lanes hold a group
-        const int v = tx + u * kFewPrepThreads;
-        const __nv_bfloat16* xb = reinterpret_cast<const __nv_bfloat16*>(&xv[u]);
+      const int xchunk = few_xchunk<true>(16);
+      if (P.xq) {
+        const int ng = D / kMxGroup;
+        if (v < (D >> 4))
+          *reinterpret_cast<uint4*>(P.xb + (v >> 3) * xchunk + swz128(c, v & 7)) =
+              __ldg(reinterpret_cast<const uint4*>(P.xq) + static_cast<size_t>(c) * (D >> 4) + v);
+        if (v < ng) P.xb[(v >> 2) * xchunk + 16 * 128 + 16 * c + (v & 3)] = __ldg(P.xs + static_cast<size_t>(c) * ng + v);
+      } else {
+        const uint4 q = v < nvec ? load_x(c, v) : make_uint4(0, 0, 0, 0);
+        const __nv_bfloat16* b = reinterpret_cast<const __nv_bfloat16*>(&q);
         float f[8];
         uint32_t m = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          f[j] = __bfloat162float(xb[j]);
+          f[j] = __bfloat162float(b[j]);
           m = max(m, abs_bits(f[j]));
         }
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));  // four lanes hold a group
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
         const uint32_t sc = mx_scale_code(m);
         const float inv = mx_inv_scale(sc);
         if (v < nvec) {
           uint8_t* at = P.xb + (v >> 4) * xchunk;
-          *reinterpret_cast<uint2*>(at + swz128(t, (v >> 1) & 7) + (v & 1) * 8) =
+          *reinterpret_cast<uint2*>(at + swz128(c, (v >> 1) & 7) + (v & 1) * 8) =
               make_uint2(e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
                          e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
-          if ((v & 3) == 0) at[16 * 128 + 16 * t + ((v >> 2) & 3)] = static_cast<uint8_t>(sc);
+          if ((v & 3) == 0) at[16 * 128 + 16 * c + ((v >> 2) & 3)] = static_cast<uint8_t>(sc);
         }
       }
     }
+  }
+  if (!route) return;
+  for (int i = tx; i < P.T * (kFewRouterRows / 8); i += kFewPrepThreads) {
+    const int t = i / (kFewRouterRows / 8), v = i % (kFewRouterRows / 8);
+    const uint4 q = k0 + v * 8 < D ? load_x(t, (k0 >> 3) + v) : make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(&s_x[t][v * 8]) = q;
+  }
+  __syncthreads();
+  for (int t0 = 0; t0 < P.T; t0 += kTB) {
+    float4 acc[kTB];
+#pragma unroll
+    for (int j = 0; j < kTB; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kRowsPer; ++i) {
+      const float w0 = __uint_as_float(w[i].x << 16), w1 = __uint_as_float(w[i].x & 0xFFFF0000u);
+      const float w2 = __uint_as_float(w[i].y << 16), w3 = __uint_as_float(w[i].y & 0xFFFF0000u);
+#pragma unroll
+      for (int j = 0; j < kTB; ++j) {  // (rows of s_x past T hold anything; their sums are not stored)
+        const float x = __bfloat162float(s_x[t0 + j][warp * kRowsPer + i]);
+        acc[j].x = fmaf(x, w0, acc[j].x);
+        acc[j].y = fmaf(x, w1, acc[j].y);
+        acc[j].z = fmaf(x, w2, acc[j].z);
+        acc[j].w = fmaf(x, w3, acc[j].w);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kTB; ++j) s_part[warp][j][lane] = acc[j];
+    __syncthreads();
+    if (tx < kTB * 32 && t0 + (tx >> 5) < P.T) {
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int g = 0; g < kWarps; ++g) {
+        const float4 b = s_part[g][tx >> 5][lane];
+        a.x += b.x;
+        a.y += b.y;
+        a.z += b.z;
+        a.w += b.w;
+      }
+      reinterpret_cast<float4*>(P.logit_part)[(c * 16 + t0 + (tx >> 5)) * 32 + lane] = a;
+    }
+    __syncthreads();
   }
 }
 
@@ -368,7 +415,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   uint64_t* acc_full = empty + kFewMaxStages;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* routed = acc_empty + 2;
-  uint64_t* drain = routed + 1;
+  uint64_t* weighted = routed + 1;  // the routing's second half: weights and masks
+  uint64_t* drain = weighted + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   uint32_t* sTouched = tmem_slot + 1;  // [4] bitmask of experts
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sTouched + 4);
@@ -377,15 +425,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x, grid = gridDim.x;
-  const int nr = (D + kFewRouterRows - 1) / kFewRouterRows;  // router CTAs (at most 16: the grid is larger)
+  const int nr = (D + kFewRouterRows - 1) / kFewRouterRows;  // parts of the logits
   const int ks_dn = (P.S + kKC - 1) / kKC, ke_dn = (P.F + kKC - 1) / kKC;
   const int su = (P.S + kFewGuCols - 1) / kFewGuCols, fu = (P.F + kFewGuCols - 1) / kFewGuCols;
   const int nd = (D + kFewDnCols - 1) / kFewDnCols;
-  uint32_t* c_router = P.counters;
-  uint32_t* c_hidden = P.counters + 1;
-  uint32_t* c_down = P.counters + 2;
-  uint32_t* c_shared = P.counters + 3;
-  uint32_t* c_rows = P.counters + 4;
+  uint32_t* c_hidden = P.counters;
+  uint32_t* c_down = P.counters + 1;
+  uint32_t* c_shared = P.counters + 2;
+  uint32_t* c_rows = P.counters + 3;
   uint32_t* c_eu = P.counters + 8;
 
   if (threadIdx.x == 0) {
@@ -399,6 +446,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
       mbar_init(&acc_empty[b], kFewConsWarps);
     }
     mbar_init(routed, 1);
+    mbar_init(weighted, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     *sCount = 0;
@@ -469,15 +517,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     } else if (role == 1) {
       tma_prefetch_desc(&P.tmSu);
       tma_prefetch_desc(&P.tmU);
-    }
-    if (cta < nr) {  // the router's rows: 128 experts (two boxes of 64) x 64 K per chunk
-      for (int k0 = cta * kFewRouterRows; k0 < min(D, (cta + 1) * kFewRouterRows); k0 += 64) {
-        if (!acquire()) break;
-        if (role == 0) mbar_arrive_expect_tx(&full[s], 2 * 8192 + rows * 128);
-        if (role < 2) tma_load_3d(ring + s * stage_bytes + role * 8192, &P.tmR, &full[s], role * 64, k0, 0);
-        if (role == 4) bulk_load(ring + s * stage_bytes + kHOff, P.xr + k0 / 64 * rows * 128, rows * 128, &full[s]);
-        advance();
-      }
     }
     for (int i = sBegS[cta], e = sBegS[cta + 1]; i < e; ++i) {
       if (!ok || !acquire()) break;
@@ -622,24 +661,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
           end_acc();
         }
       };
-      if (cta < nr) {  // R
-        const int k0 = cta * kFewRouterRows, k1 = min(D, k0 + kFewRouterRows);
-        const uint32_t d = begin_acc();
-        for (int k = k0; ok && k < k1; k += 64) {
-          if (!mbar_wait_cycles(&full[s], ph, abort_flag, P.err)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          const uint32_t a = smem_u32(ring + s * stage_bytes), b = a + kHOff;
-          const uint32_t al = desc_lo(a, 8192), bl = desc_lo(b, 16);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            few_umma_bf16(d, al + j * 128, desc_hi(1024), bl + j * 2, xhi, few_idesc_bf16(16), k != k0 || j != 0);
-          end_chunk();
-        }
-        end_acc();
-      }
       run_gu(sBegS);
       if (ok && !mbar_wait_cycles(routed, 0, abort_flag, P.err)) ok = false;
       if (ok) {
@@ -699,135 +720,144 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     // ------------------------------------------------------------- routing
     const int wr = wx - kFewConsWarps;  // 0..7: tokens wr, wr + 8
     const int rt = wr * 32 + lane;
-    for (int i = rt; i < 128 * 16; i += 256) sW[i] = 0.f;
-    if (rt < 128) sBits[rt] = 0;
-    if (wr < P.T) {  // warps with tokens
-      int got = 0;
-      if (lane == 0) got = counter_wait(c_router, nr, abort_flag, P.err);
-      got = __shfl_sync(0xffffffffu, got, 0);  // (a wait that gave up has raised abort)
-      if (got) {
-        // tokens wr and wr + 8 (if there) side by side; this lane's experts 4 lane .. 4 lane + 3
-        const int ntok = wr + 8 < P.T ? 2 : 1;
-        const int e4 = lane * 4;
-        const bool in = e4 < P.E;
-        float l[2][4] = {};
-        for (int r0 = 0; r0 < nr; r0 += 4) {  // the partial logits in CTA order
-          float4 v[2][4];
+    if (wr < P.T) {
+      // tokens wr and wr + 8 (if there) side by side; this lane's experts 4 lane .. 4 lane + 3
+      const int ntok = wr + 8 < P.T ? 2 : 1;
+      const int e4 = lane * 4;
+      const bool in = e4 < P.E;
+      float l[2][4] = {};
+      const float4* parts = reinterpret_cast<const float4*>(P.logit_part) + wr * 32 + lane;
+      auto add_part = [&](float (&a)[4], const float4& v) {
+        a[0] += v.x;
+        a[1] += v.y;
+        a[2] += v.z;
+        a[3] += v.w;
+      };
+      const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (ntok == 1) {
+        for (int r0 = 0; r0 < nr; r0 += 12) {  // the partial logits in order
+          float4 v[12];
+#pragma unroll
+          for (int r = 0; r < 12; ++r) v[r] = r0 + r < nr ? __ldcg(parts + (r0 + r) * 16 * 32) : zero;
+#pragma unroll
+          for (int r = 0; r < 12; ++r) add_part(l[0], v[r]);
+        }
+      } else {
+        for (int r0 = 0; r0 < nr; r0 += 6) {
+          float4 v[2][6];
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-              v[h][r] = r0 + r < nr && h < ntok
-                            ? __ldcg(reinterpret_cast<const float4*>(P.logit_part) + ((r0 + r) * 16 + wr + 8 * h) * 32 + lane)
-                            : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int r = 0; r < 6; ++r) v[h][r] = r0 + r < nr ? __ldcg(parts + ((r0 + r) * 16 + 8 * h) * 32) : zero;
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              l[h][0] += v[h][r].x;
-              l[h][1] += v[h][r].y;
-              l[h][2] += v[h][r].z;
-              l[h][3] += v[h][r].w;
+            for (int r = 0; r < 6; ++r) add_part(l[h], v[h][r]);
+        }
+      }
+      uint32_t key[2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (in && P.bias) l[h][i] += __ldg(P.bias + e4 + i);
+          key[h][i] = in ? max(order_key(l[h][i] + 0.f), 1u) : 0u;  // (-0 + 0 = +0); key 0: not to be taken
+          if (in && h < ntok && cta == 0 && P.logits_out)
+            P.logits_out[static_cast<size_t>(wr + 8 * h) * P.E + e4 + i] = l[h][i];
+        }
+      // k rounds of: the largest key, the lowest expert among equals; slot j stays in lane j
+      uint32_t my_key[2] = {0, 0};
+      int my_e[2] = {0, 0};
+      for (int j = 0; j < P.k; ++j) {
+        uint32_t bk[2], top[2];
+        int be[2], e[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          bk[h] = key[h][0];
+          be[h] = e4;
+#pragma unroll
+          for (int i = 1; i < 4; ++i)
+            if (key[h][i] > bk[h]) {
+              bk[h] = key[h][i];
+              be[h] = e4 + i;
             }
         }
-        uint32_t key[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) top[h] = __reduce_max_sync(0xffffffffu, bk[h]);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
+          e[h] = static_cast<int>(
+              __reduce_min_sync(0xffffffffu, bk[h] == top[h] ? static_cast<uint32_t>(be[h]) : 0xFFFFu));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (in && P.bias) l[h][i] += __ldg(P.bias + e4 + i);
-            key[h][i] = in ? max(order_key(l[h][i] + 0.f), 1u) : 0u;  // (-0 + 0 = +0); key 0: not to be taken
-            if (in && h < ntok && cta == 0 && P.logits_out)
-              P.logits_out[static_cast<size_t>(wr + 8 * h) * P.E + e4 + i] = l[h][i];
-          }
-        for (int j = 0; j < P.k; ++j) {
-          // the largest key, the lowest expert among equals
-          uint32_t bk[2], top[2];
-          int be[2], e[2];
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            bk[h] = key[h][0];
-            be[h] = e4;
-#pragma unroll
-            for (int i = 1; i < 4; ++i)
-              if (key[h][i] > bk[h]) {
-                bk[h] = key[h][i];
-                be[h] = e4 + i;
-              }
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) top[h] = __reduce_max_sync(0xffffffffu, bk[h]);
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            e[h] = static_cast<int>(
-                __reduce_min_sync(0xffffffffu, bk[h] == top[h] ? static_cast<uint32_t>(be[h]) : 0xFFFFu));
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (h < ntok && e4 == (e[h] & ~3)) {
-              const int t = wr + 8 * h;
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if ((e[h] & 3) == i) {
-                  sSel[t * kFewMaxTopK + j] = l[h][i];
-                  key[h][i] = 0u;
-                }
-              sCh[t * kFewMaxTopK + j] = static_cast<uint8_t>(e[h]);
-              if (cta == 0 && P.idx_out) P.idx_out[static_cast<size_t>(t) * P.k + j] = e[h];
-              if (e[h] >= P.e0 && e[h] < P.e0 + P.el) atomicOr(&sTouched[e[h] >> 5], 1u << (e[h] & 31));
-            }
-        }
-        __syncwarp();
-        for (int h = 0; h < ntok; ++h) {
-          // softmax over the kept logits (slot 0 holds the largest), slot `lane`
-          const int t = wr + 8 * h;
-          const float mx = sSel[t * kFewMaxTopK];
-          const float ex = lane < P.k ? expf(sSel[t * kFewMaxTopK + lane] - mx) : 0.f;
-          float sum = ex;
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          __syncwarp();
-          if (lane < P.k) {
-            sSel[t * kFewMaxTopK + lane] = ex / sum;
-            if (cta == 0 && P.w_out) P.w_out[static_cast<size_t>(t) * P.k + lane] = ex / sum;
+          for (int i = 0; i < 4; ++i)
+            if (e4 + i == e[h]) key[h][i] = 0u;
+          if (lane == j) {
+            my_key[h] = top[h];
+            my_e[h] = e[h];
           }
         }
       }
+      for (int h = 0; h < ntok; ++h) {
+        const int t = wr + 8 * h;
+        // the key's logit; softmax over the kept ones (slot 0 holds the largest)
+        const float logit = __uint_as_float((my_key[h] & 0x80000000u) ? my_key[h] ^ 0x80000000u : ~my_key[h]);
+        const float mx = __shfl_sync(0xffffffffu, logit, 0);
+        const float ex = lane < P.k ? expf(logit - mx) : 0.f;
+        float sum = ex;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane < P.k) {
+          const int e = my_e[h];
+          sSel[t * kFewMaxTopK + lane] = ex / sum;
+          sCh[t * kFewMaxTopK + lane] = static_cast<uint8_t>(e);
+          if (e >= P.e0 && e < P.e0 + P.el) atomicOr(&sTouched[e >> 5], 1u << (e & 31));
+          if (cta == 0 && P.w_out) P.w_out[static_cast<size_t>(t) * P.k + lane] = ex / sum;
+          if (cta == 0 && P.idx_out) P.idx_out[static_cast<size_t>(t) * P.k + lane] = e;
+        }
+      }
     }
+    for (int i = rt; i < 128 * 16; i += 256) sW[i] = 0.f;
+    if (rt < 128) sBits[rt] = 0;
     bar_named(2, 32 * kFewConsWarps);
-    const bool ok = *abort_flag == 0;
-    // the list of touched experts, ascending
+    // the list of touched experts, ascending, and the ranges: what the copying threads need
+    const uint32_t touched[4] = {sTouched[0], sTouched[1], sTouched[2], sTouched[3]};
     auto position = [&](int e) -> int {
-      int pos = __popc(sTouched[e >> 5] & ((1u << (e & 31)) - 1u));
-      for (int i = 0; i < (e >> 5); ++i) pos += __popc(sTouched[i]);
+      int pos = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        pos += i < (e >> 5) ? __popc(touched[i]) : i == (e >> 5) ? __popc(touched[i] & ((1u << (e & 31)) - 1u)) : 0;
       return pos;
     };
+    const int n = __popc(touched[0]) + __popc(touched[1]) + __popc(touched[2]) + __popc(touched[3]);
     if (rt < 128 && ((sTouched[rt >> 5] >> (rt & 31)) & 1u)) sList[position(rt)] = static_cast<uint8_t>(rt - P.e0);
-    if (rt == 0) *sCount = __popc(sTouched[0]) + __popc(sTouched[1]) + __popc(sTouched[2]) + __popc(sTouched[3]);
+    if (rt == 0) *sCount = n;
+    const int len = ks_dn + n * ke_dn;
+    const FewSplit sd(nd * len, grid);
     if (rt <= grid) {
-      const int n = __popc(sTouched[0]) + __popc(sTouched[1]) + __popc(sTouched[2]) + __popc(sTouched[3]);
       sBegE[rt] = FewSplit(n * fu * ck, grid).begin(rt);
-      const int len = ks_dn + n * ke_dn;
-      const FewSplit sd(nd * len, grid);
       sBegD[rt] = sd.begin(rt);
-      if (rt < nd) {
-        sTileA[rt] = sd.cta_of(rt * len);
-        sTileB[rt] = sd.cta_of((rt + 1) * len - 1);
-      }
-    }
-    if (ok) {
-      for (int a = rt; a < kFewMaxTokens * kFewMaxTopK; a += 256) {
-        const int t = a / kFewMaxTopK, j = a % kFewMaxTopK;
-        if (t >= P.T || j >= P.k) continue;
-        const int e = sCh[a];
-        if (e < P.e0 || e >= P.e0 + P.el) continue;
-        const int pos = position(e);
-        sW[pos * 16 + t] = sSel[a];
-        atomicOr(&sBits[pos], 1u << t);
-      }
     }
     bar_named(2, 32 * kFewConsWarps);
-    if (rt == 0 && ok) mbar_arrive(routed);
-    if (ok && cta == 0 && P.cnt_out && rt < P.E)
+    if (rt == 0) mbar_arrive(routed);
+    // what the consumers need: weights, masks, the CTAs of each output tile
+    if (rt < nd) {
+      sTileA[rt] = sd.cta_of(rt * len);
+      sTileB[rt] = sd.cta_of((rt + 1) * len - 1);
+    }
+    for (int a = rt; a < kFewMaxTokens * kFewMaxTopK; a += 256) {
+      const int t = a / kFewMaxTopK, j = a % kFewMaxTopK;
+      if (t >= P.T || j >= P.k) continue;
+      const int e = sCh[a];
+      if (e < P.e0 || e >= P.e0 + P.el) continue;
+      const int pos = position(e);
+      sW[pos * 16 + t] = sSel[a];
+      atomicOr(&sBits[pos], 1u << t);
+    }
+    bar_named(2, 32 * kFewConsWarps);
+    if (rt == 0) mbar_arrive(weighted);
+    if (cta == 0 && P.cnt_out && rt < P.E)
       P.cnt_out[rt] = ((sTouched[rt >> 5] >> (rt & 31)) & 1u) ? __popc(sBits[position(rt)]) : 0;
     return;
   }
@@ -868,21 +898,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     }
     return before;
   };
-  // ---- R: partial logits of 256 K rows; expert `col`, eight tokens per half
-  if (cta < nr) {
-    wait_acc();
-    uint32_t a[8];
-    tmem_ld_32x32b_x8(tlane + half * 8, a);
-    free_acc();
-    if (ok) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (half * 8 + j < P.T)
-          P.logit_part[(static_cast<size_t>(cta) * 16 + half * 8 + j) * 128 + col] = __uint_as_float(a[j]);
-    }
-    publish(c_router);
-  }
-
   // ---- S, E: a unit's sums (this thread: column `col`, tokens 8 half ..) come from one CTA, or as parts from several,
   // each part in its CTA's slot of part_gu. The shared MLP's GeGLU rows are made by all CTAs while the first experts'
   // weights arrive; an expert unit's by the last of its CTAs.
@@ -943,7 +958,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   }
   publish(c_shared);
   if (ct == 0)
-    *sLast = mbar_wait_cycles(routed, 0, abort_flag, P.err) && counter_wait(c_shared, grid, abort_flag, P.err) ? 1 : 0;
+    *sLast = mbar_wait_cycles(weighted, 0, abort_flag, P.err) && counter_wait(c_shared, grid, abort_flag, P.err) ? 1 : 0;
   bar_named(1, 32 * kFewConsWarps);
   const bool go = *sLast != 0;  // without a routing all eight warps stop here (the wait has raised abort)
   bar_named(1, 32 * kFewConsWarps);

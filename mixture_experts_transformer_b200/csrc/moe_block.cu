@@ -1026,7 +1026,8 @@ moe_status enqueue_block_mx(const moe_mxfp8_params* p, const Dims& d, const MxLa
   {
     const int blocks = static_cast<int>(std::min<long long>((d.T + 7LL) / 8, 148LL * 64));  // a warp per token
     LaunchScope ls_(kKScatterMx, st);
-    MOE_TRY(ls_.done(launch_k(route_scatter_mx_kernel, blocks, 256, 0, st, idx, masks, base, d.T, d.k, d.E, d.D,
+    const int share = (d.D / kMxGroup + 31) / 32;  // warps' worth of groups in a row
+    MOE_TRY(ls_.done(launch_k(route_scatter_mx_kernel, dim3(blocks, std::min(share, 4)), 256, 0, st, idx, masks, base, d.T, d.k, d.E, d.D,
                               static_cast<const __nv_bfloat16*>(p->x), static_cast<const uint8_t*>(p->xq),
                               static_cast<const uint8_t*>(p->xs), row_of, ws + M.xq_perm, ws + M.xsf_perm,
                               ws + M.xq_tok, ws + M.xsf_tok, rp, s->err)));
@@ -1037,6 +1038,8 @@ moe_status enqueue_block_mx(const moe_mxfp8_params* p, const Dims& d, const MxLa
   MxParams gu;
   std::memset(&gu, 0, sizeof(gu));
   if (!map_2d_u8(&gu.tmA[0], ws + M.xq_perm, rp, d.D) || !map_2d_u8(&gu.tmAs[0], ws + M.xq_perm, rp, d.D, kMxASmallRows) ||
+      !map_2d_u8(&gu.tmAm[0], ws + M.xq_perm, rp, d.D, kMxAMidRows) ||
+      !map_2d_u8(&gu.tmAm[1], xtok, d.T, d.D, kMxAMidRows) ||
       !map_3d_u8(&gu.tmB0[0], p->wg.q, d.E, d.F, d.D) || !map_3d_u8(&gu.tmB1[0], p->wu.q, d.E, d.F, d.D) ||
       !map_2d_u8(&gu.tmA[1], xtok, d.T, d.D) || !map_2d_u8(&gu.tmAs[1], xtok, d.T, d.D, kMxASmallRows) ||
       !map_3d_u8(&gu.tmB0[1], p->sg.q, 1, d.S, d.D) || !map_3d_u8(&gu.tmB1[1], p->su.q, 1, d.S, d.D))
@@ -1050,13 +1053,14 @@ moe_status enqueue_block_mx(const moe_mxfp8_params* p, const Dims& d, const MxLa
   gu.err = s->err;
   {
     LaunchScope ls_(kKMxGateUp, st);
-    MOE_TRY(ls_.done(
-        launch_k(mx_gemm_kernel<true>, std::min(s->sm_count, L.max_tiles_gu), kMxThreads, kMxSmemBytes, st, gu)));
+    const int grid = std::min(s->sm_count, L.max_tiles_gu);
+    MOE_TRY(ls_.done(launch_k(mx_gemm_kernel<true>, grid, kMxThreads, kMxSmemBytes, st, gu)));
   }
 
   MxParams dn;
   std::memset(&dn, 0, sizeof(dn));
-  if (!map_2d_u8(&dn.tmA[0], ws + M.hq, rp, d.F) || !map_2d_u8(&dn.tmAs[0], ws + M.hq, rp, d.F, kMxASmallRows) ||
+  if (!map_2d_u8(&dn.tmAm[0], ws + M.hq, rp, d.F, kMxAMidRows) || !map_2d_u8(&dn.tmAm[1], ws + M.hsq, tp, d.S, kMxAMidRows) ||
+      !map_2d_u8(&dn.tmA[0], ws + M.hq, rp, d.F) || !map_2d_u8(&dn.tmAs[0], ws + M.hq, rp, d.F, kMxASmallRows) ||
       !map_2d_u8(&dn.tmA[1], ws + M.hsq, tp, d.S) || !map_2d_u8(&dn.tmAs[1], ws + M.hsq, tp, d.S, kMxASmallRows) ||
       !map_3d_u8(&dn.tmB0[0], p->wd.q, d.E, d.D, d.F) || !map_3d_u8(&dn.tmB0[1], p->sd.q, 1, d.D, d.S) ||
       !map_3d_u8(&dn.tmBw[0], p->wd.q, d.E, d.D, d.F, 256) || !map_3d_u8(&dn.tmBw[1], p->sd.q, 1, d.D, d.S, 256))
@@ -1071,8 +1075,8 @@ moe_status enqueue_block_mx(const moe_mxfp8_params* p, const Dims& d, const MxLa
   dn.err = s->err;
   {
     LaunchScope ls_(kKMxDown, st);
-    MOE_TRY(ls_.done(
-        launch_k(mx_gemm_kernel<false>, std::min(s->sm_count, L.max_tiles_dn), kMxThreads, kMxSmemBytes, st, dn)));
+    const int grid = std::min(s->sm_count, L.max_tiles_dn);
+    MOE_TRY(ls_.done(launch_k(mx_gemm_kernel<false>, grid, kMxThreads, kMxSmemBytes, st, dn)));
   }
   {
     LaunchScope ls_(kKCombine, st);
@@ -1094,7 +1098,7 @@ moe_status enqueue_block_mx(const moe_mxfp8_params* p, const Dims& d, const MxLa
 // ---------------------------------------------------- the layer for a few tokens
 
 struct FewLayout {
-  size_t counters, logit_part, xb, xr, h, part_gu, part_dn, f, guard, total;
+  size_t counters, logit_part, xb, h, part_gu, part_dn, f, guard, total;
   int ncounters;
 };
 
@@ -1120,7 +1124,6 @@ FewLayout make_few_layout(const Dims& d, bool mx) {
   L.logit_part = take(units(d.D, kFewRouterRows) * 16 * 128 * 4);
   const size_t rows = mx ? few_rows<true>(d.T) : few_rows<false>(d.T);
   L.xb = take(units(d.D, static_cast<int>(kc)) * (mx ? few_xchunk<true>(16) : rows * 128));
-  L.xr = mx ? take(static_cast<size_t>(d.D) / 64 * rows * 128) : L.xb;
   L.h = take(((d.S + kc - 1) / kc + act * ((d.F + kc - 1) / kc)) * hc);
   L.part_gu = take(static_cast<size_t>(kFewMaxCtas) * 2 * 2 * 2 * 16 * kFewGuCols * 4);
   L.part_dn = take(static_cast<size_t>(kFewMaxCtas) * 2 * 16 * kFewDnCols * 4);
@@ -1168,13 +1171,13 @@ moe_status enqueue_few(FewParams* P, const Dims& d, const FewLayout& L, uint8_t*
   P->part_dn = reinterpret_cast<float*>(ws + L.part_dn);
   P->f = reinterpret_cast<float*>(ws + L.f);
   P->xb = ws + L.xb;
-  P->xr = ws + L.xr;
   P->ncounters = L.ncounters;
   P->err = s->err;
   {
     LaunchScope ls_(kKFewPrep, st);
-    MOE_TRY(ls_.done(mx ? launch_k(few_prep_kernel<true>, d.T, kFewPrepThreads, 0, st, *P)
-                        : launch_k(few_prep_kernel<false>, d.T, kFewPrepThreads, 0, st, *P)));
+    const int ctas = std::max(d.T, (d.D + kFewRouterRows - 1) / kFewRouterRows);
+    MOE_TRY(ls_.done(mx ? launch_k(few_prep_kernel<true>, ctas, kFewPrepThreads, 0, st, *P)
+                        : launch_k(few_prep_kernel<false>, ctas, kFewPrepThreads, 0, st, *P)));
   }
   LaunchScope ls_(kKFew, st);
   return ls_.done(mx ? launch_few<true>(P, s->sm_count, st) : launch_few<false>(P, s->sm_count, st));
@@ -1188,13 +1191,14 @@ moe_status enqueue_few_bf16(const moe_params* p, const Dims& d, const FewLayout&
   // A row of 128 columns is 256 bytes, but starts on a 256-byte boundary only in every other row of a 704-wide matrix:
   // promoting its sectors to 256-byte fetches read 30% more from HBM than the weights hold.
   const CUtensorMapL2promotion promo = CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
-  if (!map_3d(&P.tmR, p->w_router, 1, d.D, d.E) || !map_4d_chunks(&P.tmG, p->wg, d.el, d.D, d.F, gu_blocks, promo) ||
+  if (!map_4d_chunks(&P.tmG, p->wg, d.el, d.D, d.F, gu_blocks, promo) ||
       !map_4d_chunks(&P.tmU, p->wu, d.el, d.D, d.F, gu_blocks, promo) ||
       !map_4d_chunks(&P.tmD, p->wd, d.el, d.F, d.D, dn_blocks) ||
       !map_4d_chunks(&P.tmSg, p->sg, 1, d.D, d.S, gu_blocks, promo) ||
       !map_4d_chunks(&P.tmSu, p->su, 1, d.D, d.S, gu_blocks, promo) ||
       !map_4d_chunks(&P.tmSd, p->sd, 1, d.S, d.D, dn_blocks))
     return MOE_ERR_CUDA;
+  P.w_router = static_cast<const __nv_bfloat16*>(p->w_router);
   P.x = static_cast<const __nv_bfloat16*>(p->x);
   P.norm_pre = static_cast<const __nv_bfloat16*>(p->norm_pre);
   P.norm_post = static_cast<const __nv_bfloat16*>(p->norm_post);
@@ -1231,7 +1235,7 @@ moe_status enqueue_few_mx(const moe_mxfp8_params* p, const Dims& d, const FewLay
                           cudaStream_t st) {
   FewParams P;
   std::memset(&P, 0, sizeof(P));
-  if (!map_3d(&P.tmR, p->w_router, 1, d.D, d.E) || !map_3d_u8(&P.tmG, p->wg.q, d.E, d.F, d.D, kFewGuCols) ||
+  if (!map_3d_u8(&P.tmG, p->wg.q, d.E, d.F, d.D, kFewGuCols) ||
       !map_3d_u8(&P.tmU, p->wu.q, d.E, d.F, d.D, kFewGuCols) ||
       !map_3d_u8(&P.tmD, p->wd.q, d.E, d.D, d.F, kFewDnCols) ||
       !map_3d_u8(&P.tmSg, p->sg.q, 1, d.S, d.D, kFewGuCols) || !map_3d_u8(&P.tmSu, p->su.q, 1, d.S, d.D, kFewGuCols) ||
@@ -1243,6 +1247,7 @@ moe_status enqueue_few_mx(const moe_mxfp8_params* p, const Dims& d, const FewLay
   P.sfsg = p->sg.sf;
   P.sfsu = p->su.sf;
   P.sfsd = p->sd.sf;
+  P.w_router = static_cast<const __nv_bfloat16*>(p->w_router);
   P.x = static_cast<const __nv_bfloat16*>(p->x);
   P.xq = static_cast<const uint8_t*>(p->xq);
   P.xs = static_cast<const uint8_t*>(p->xs);

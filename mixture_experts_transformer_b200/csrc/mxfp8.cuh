@@ -10,9 +10,11 @@
 // The GEMM (mx_gemm_kernel) has the NVFP4 GEMM's structure with
 // `tcgen05.mma.kind::mxf8f6f4.block_scale.block32`: one 128-K stage is 128
 // bytes of every operand row and exactly one scale atom per 128-row block, so
-// a stage's scales are one 512-byte copy each and go to one TMEM slot; the four
-// 32-K MMAs of the stage pick their byte of the slot's words by the scale id of
-// the instruction descriptor. A reduction that ends inside a stage (K a multiple
+// a stage's scales are one 512-byte copy each; the MMA thread copies them to the
+// stage's TMEM slot (tcgen05.cp) ahead of its MMAs - scale warps as in the NVFP4
+// GEMM, whose stages hold four times the atoms, cost more than they saved (T = 64
+// 200 -> 193 us without). The four 32-K MMAs of the stage pick their byte of the
+// slot's words by the scale id of the instruction descriptor. A reduction that ends inside a stage (K a multiple
 // of 64) issues only the MMAs it has.
 #pragma once
 
@@ -82,7 +84,9 @@ __global__ void mx_act_quant_kernel(const __nv_bfloat16* __restrict__ x, size_t 
 // from xq / xs (codes [T][D], scales [T][D/32]); each lane handles whole
 // groups. Written: the codes and scale atoms of the token's k routed rows, the
 // token-order scale atoms (the shared MLP's), and - without xq, which the shared
-// MLP reads in place - the token-order codes.
+// MLP reads in place - the token-order codes. The blocks of a grid column (y) take
+// every gridDim.y-th 32 groups: large batches have three, as one warp per token left
+// too few loads in flight (T = 4096 38 us).
 __global__ void __launch_bounds__(256) route_scatter_mx_kernel(
     const int32_t* __restrict__ idx, const uint32_t* __restrict__ masks, const int32_t* __restrict__ base, int T,
     int k, int E, int D, const __nv_bfloat16* __restrict__ x, const uint8_t* __restrict__ xq,
@@ -106,13 +110,13 @@ __global__ void __launch_bounds__(256) route_scatter_mx_kernel(
           atomicOr(err, kErrBadIndex);
           row = -1;
         } else {
-          row_of[a] = row;
+          if (blockIdx.y == 0) row_of[a] = row;
         }
       }
       s_rows[wid][j] = row;
     }
     __syncwarp();
-    for (int g0 = 0; g0 < ng; g0 += 32) {
+    for (int g0 = blockIdx.y * 32; g0 < ng; g0 += 32 * gridDim.y) {
       const int g = g0 + lane;
       const bool in = g < ng;
       uint4 codes[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
@@ -158,13 +162,16 @@ __global__ void __launch_bounds__(256) route_scatter_mx_kernel(
 
 constexpr int kMxKStage = 128;                    // K elements (= bytes of a row) per stage
 constexpr int kMxABytes = 128 * kMxKStage;        // 128 rows
-constexpr int kMxBBytes = 2 * 128 * kMxKStage;    // two 128-row blocks
 constexpr int kMxSfBytes = 512;                   // one atom per 128-row block
+constexpr int kMxProd1 = 10;                      // warps of copying threads 1 and 2 (thread 0: warp 0)
+constexpr int kMxThreads = 32 * (kMxProd1 + 2);   // copy, MMA, 8 epilogue, 2 copy warps
+constexpr int kMxASmallRows = 32;                 // rows of the small A boxes
+constexpr int kMxAMidRows = 64;
+constexpr int kMxBBytes = 2 * 128 * kMxKStage;    // two 128-row blocks
 constexpr int kMxStages = 4;
-constexpr int kMxThreads = 320 + 128;             // producer, MMA, 8 epilogue warps, 4 scale warps
-constexpr int kMxASmallRows = 32;                 // rows of the small A box
+constexpr int kMxStgWarpBytes = 2048;             // epilogue staging per warp (32 rows x 64 B)
 constexpr int kMxSmemBytes =
-    kMxStages * (kMxABytes + kMxBBytes + 3 * kMxSfBytes) + 8 * kF4StgWarpBytes + 1024 + 512;
+    kMxStages * (kMxABytes + kMxBBytes + 3 * kMxSfBytes) + 8 * kMxStgWarpBytes + 1024 + 512;
 
 struct MxProblem {
   int K;          // multiple of 64
@@ -182,7 +189,8 @@ struct MxProblem {
 
 struct MxParams {
   CUtensorMap tmA[2];   // codes [rows][K] u8, box 128 x 128, 128-byte swizzle
-  CUtensorMap tmAs[2];  // the same, box 128 x 32: tiles of at most 32 rows copy only those
+  CUtensorMap tmAs[2];  // the same, boxes 128 x 32 and 128 x 64: tiles of at most as many rows copy only those
+  CUtensorMap tmAm[2];
   CUtensorMap tmB0[2];  // codes [groups][N][K] u8, box 128 x 128 x 1
   CUtensorMap tmB1[2];
   CUtensorMap tmBw[2];  // down: box 128 x 256 x 1
@@ -215,6 +223,15 @@ __device__ __forceinline__ void umma_mxf8(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
+// A 512-byte scale tile from shared memory into 4 TMEM columns of every lane quarter (row i of 16 bytes to lane i).
+// In order with this thread's MMAs. The column has to be a multiple of 4. Descriptor: no swizzle, 8-row groups 128 bytes apart.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t saddr) {
+  asm volatile(
+      "{\n\t.reg .b64 a;\n\tmov.b64 a, {%1, %2};\n\ttcgen05.cp.cta_group::1.32x128b.warpx4 [%0], a;\n\t}" ::"r"(taddr),
+      "r"(saddr >> 4), "r"((128u >> 4) | (1u << 14))
+      : "memory");
+}
+
 // TMEM columns [0, 256): the accumulator (GATEUP: gate 0..127, up 128..255;
 // DOWN: output columns n0 .. n0+255); from 256: one scale slot per stage, A
 // scales at +0, B block 0 at +4, B block 1 at +8.
@@ -226,13 +243,12 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
   uint8_t* sB = sA + kMxStages * kMxABytes;
   uint8_t* sSf = sB + kMxStages * kMxBBytes;  // per stage: A atom, B block 0 atom, B block 1 atom
   uint8_t* sStg = sSf + kMxStages * 3 * kMxSfBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sStg + 8 * kF4StgWarpBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sStg + 8 * kMxStgWarpBytes);
   uint64_t* empty = full + kMxStages;
   uint64_t* acc_full = empty + kMxStages;
   uint64_t* acc_empty = acc_full + 1;
   uint64_t* drain = acc_empty + 1;
-  uint64_t* sf_ready = drain + 1;  // a stage's scale atoms are in TMEM (one arrival per scale warp)
-  uint64_t* tile_full = sf_ready + kMxStages;
+  uint64_t* tile_full = drain + 1;
   uint64_t* tile_empty = tile_full + kTileRing;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tile_empty + kTileRing);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -244,14 +260,13 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
     for (int s = 0; s < kMxStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&sf_ready[s], 4);
     }
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, 8);  // one arrival per epilogue warp
     mbar_init(drain, 1);
     for (int r = 0; r < kTileRing; ++r) {
       mbar_init(&tile_full[r], 1);
-      mbar_init(&tile_empty[r], 1 + 8 + 4);  // MMA thread, epilogue and scale warps read each index
+      mbar_init(&tile_empty[r], 1 + 8 + 2);  // MMA thread, epilogue and copy warps read each index
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -324,15 +339,11 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
         const int next = atomicAdd(P.next_tile, 1);  // its latency hides behind this tile's loads
         const MxProblem& pr = P.prob[p];
         const int kb = mx_kblocks(pr.K);
-        const int nbr = (pr.N + 127) / 128;
-        const int nb0 = tile.n0 >> 7;
-        const int nb1 = GATEUP ? nb0 : nb0 + 1;
         const uint8_t* sfa = pr.sfa + static_cast<size_t>(tile.row0 >> 7) * kb * 512;
-        const uint8_t* sfb0 = pr.sfb0 + (static_cast<size_t>(g) * nbr + nb0) * kb * 512;
-        const uint8_t* sfb1 = (GATEUP ? pr.sfb1 : pr.sfb0) + (static_cast<size_t>(g) * nbr + nb1) * kb * 512;
         const bool two_b = GATEUP || (tile.n0 + 128 < pr.N);
-        const bool small = tile.rows <= kMxASmallRows;
-        const uint32_t bytes = (small ? kMxASmallRows * kMxKStage : kMxABytes) +
+        const bool small = tile.rows <= kMxASmallRows, mid = !small && tile.rows <= kMxAMidRows;
+        const CUtensorMap* ma = small ? &P.tmAs[p] : mid ? &P.tmAm[p] : &P.tmA[p];
+        const uint32_t bytes = (small ? kMxASmallRows * kMxKStage : mid ? kMxAMidRows * kMxKStage : kMxABytes) +
                                (two_b ? 2 : 1) * (kMxBBytes / 2) + kMxSfBytes * (two_b ? 3 : 2);
         for (int ks = 0; ks < kb; ++ks) {
           if (!mbar_wait_cycles(&empty[s], ph ^ 1, abort_flag, P.err)) {
@@ -340,18 +351,8 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
             break;
           }
           mbar_arrive_expect_tx(&full[s], bytes);
-          tma_load_2d(sA + s * kMxABytes, small ? &P.tmAs[p] : &P.tmA[p], &full[s], ks * kMxKStage, tile.row0);
-          if (!GATEUP && two_b) {
-            tma_load_3d(sB + s * kMxBBytes, &P.tmBw[p], &full[s], ks * kMxKStage, tile.n0, g);  // 256 rows
-          } else {
-            tma_load_3d(sB + s * kMxBBytes, &P.tmB0[p], &full[s], ks * kMxKStage, tile.n0, g);
-            if (two_b)
-              tma_load_3d(sB + s * kMxBBytes + kMxBBytes / 2, &P.tmB1[p], &full[s], ks * kMxKStage, tile.n0, g);
-          }
-          uint8_t* sf = sSf + s * 3 * kMxSfBytes;
-          bulk_load(sf, sfa + static_cast<size_t>(ks) * 512, kMxSfBytes, &full[s]);
-          bulk_load(sf + kMxSfBytes, sfb0 + static_cast<size_t>(ks) * 512, kMxSfBytes, &full[s]);
-          if (two_b) bulk_load(sf + 2 * kMxSfBytes, sfb1 + static_cast<size_t>(ks) * 512, kMxSfBytes, &full[s]);
+          tma_load_2d(sA + s * kMxABytes, ma, &full[s], ks * kMxKStage, tile.row0);
+          bulk_load(sSf + s * 3 * kMxSfBytes, sfa + static_cast<size_t>(ks) * 512, kMxSfBytes, &full[s]);
           ++issued;
           if (++s == kMxStages) {
             s = 0;
@@ -392,7 +393,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
         tc_fence_after_sync();
         bool ok = true;
         for (int ks = 0; ks < kb; ++ks) {
-          if (!mbar_wait_cycles(&full[s], ph, abort_flag, P.err) || !mbar_wait_cycles(&sf_ready[s], ph, abort_flag, P.err)) {
+          if (!mbar_wait_cycles(&full[s], ph, abort_flag, P.err)) {
             ok = false;
             break;
           }
@@ -400,13 +401,17 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
           const int n32 = min(4, (pr.K - ks * kMxKStage) / 32);
           const uint32_t a_addr = smem_u32(sA + s * kMxABytes);
           const uint32_t b_addr = smem_u32(sB + s * kMxBBytes);
-          const uint32_t cols = tmem_base + kAccCols + s * 16;
+          // the stage's scale atoms, in order before its MMAs; the slot's last readers were done when the stage was refilled
+          const uint32_t slot = tmem_base + kAccCols + s * 16, sf = smem_u32(sSf + s * 3 * kMxSfBytes);
+          tmem_cp_scales(slot, sf);
+          tmem_cp_scales(slot + 4, sf + kMxSfBytes);
+          if (two_b) tmem_cp_scales(slot + 8, sf + 2 * kMxSfBytes);
           for (int i = 0; i < n32; ++i) {
             // 32 K of e4m3 = 32 B per row inside the 128-byte swizzled rows; both
-            // B blocks are consecutive 128-row halves of the stage and their scale
-            // words sit at +4 and +8: one MMA of N = 256 covers both
+            // B blocks are consecutive halves of the stage and their scale words
+            // sit at +4 and +8: one MMA of N = 256 covers both
             umma_mxf8(tmem_base, sdesc_sw128(a_addr + i * 32, 16, 1024), sdesc_sw128(b_addr + i * 32, 16, 1024),
-                      idesc_mxf8_m128(two_b ? 256 : 128, i), cols, cols + 4, (ks | i) != 0);
+                      idesc_mxf8_m128(two_b ? 256 : 128, i), slot, slot + 4, (ks | i) != 0);
           }
           any = true;
           umma_commit(&empty[s]);
@@ -425,45 +430,48 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
         mbar_wait_cycles(drain, 0, reinterpret_cast<volatile int*>(&dummy), P.err);
       }
     }
-  } else if (warp >= 10) {
-    // ------------------------------------------------------- scale warps
-    // As in the NVFP4 GEMM: warps 10..13 copy a stage's atoms into its TMEM
-    // slot, each its own lane quarter (row i of an atom - 16 bytes - to lane
-    // i of every quarter). Slot s is rewritten only after full[s] completed
-    // again, i.e. after the MMAs that read it.
-    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    int s = 0;
-    uint32_t ph = 0;
-    while (true) {
-      const int ti = next_tile(true);
-      if (ti < 0) break;
-      const Tile tile = P.tiles[ti];
-      const MxProblem& pr = P.prob[tile.pg >> 16];
-      const int kb = mx_kblocks(pr.K);
-      const bool two_b = GATEUP || (tile.n0 + 128 < pr.N);
+  } else if (warp >= kMxProd1) {
+    // --------------------------------------------------- copy threads 1, 2
+    // B and its scale atoms: thread 1 the gate weights (down: all 256 rows, or
+    // the only 128), thread 2 the up weights (down: the atoms). Six copies a stage
+    // from one thread took 0.6 us. A copy may land before thread 0 announces the
+    // stage's bytes; the stage completes with both.
+    if (lane == 0) {
+      const bool up = warp != kMxProd1;
+      int s = 0;
+      uint32_t ph = 0;
       bool ok = true;
-      for (int ks = 0; ks < kb; ++ks) {
-        int got = 1;
-        if (lane == 0) got = mbar_wait_cycles(&full[s], ph, abort_flag, P.err);
-        if (!__shfl_sync(0xffffffffu, got, 0)) {
-          ok = false;
-          break;
-        }
-        const uint8_t* sf = sSf + s * 3 * kMxSfBytes + lane * 16;
-        const uint32_t cols = tmem_base + lane_base + kAccCols + s * 16;
-        tmem_st_32x32b_x4(cols, *reinterpret_cast<const uint4*>(sf));
-        tmem_st_32x32b_x4(cols + 4, *reinterpret_cast<const uint4*>(sf + kMxSfBytes));
-        if (two_b) tmem_st_32x32b_x4(cols + 8, *reinterpret_cast<const uint4*>(sf + 2 * kMxSfBytes));
-        tmem_st_wait();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sf_ready[s]);
-        if (++s == kMxStages) {
-          s = 0;
-          ph ^= 1;
+      while (ok) {
+        const int ti = next_tile(false);
+        if (ti < 0) break;
+        const Tile tile = P.tiles[ti];
+        const int p = tile.pg >> 16, g = tile.pg & 0xFFFF;
+        const MxProblem& pr = P.prob[p];
+        const int kb = mx_kblocks(pr.K);
+        const size_t atom = (static_cast<size_t>(g) * ((pr.N + 127) / 128) + (tile.n0 >> 7)) * kb;
+        const bool two_b = GATEUP || (tile.n0 + 128 < pr.N);
+        const CUtensorMap* m = GATEUP ? (up ? &P.tmB1[p] : &P.tmB0[p]) : two_b ? &P.tmBw[p] : &P.tmB0[p];
+        const uint8_t* src = (GATEUP && up ? pr.sfb1 : pr.sfb0) + atom * 512;
+        for (int ks = 0; ks < kb; ++ks) {
+          if (!mbar_wait_cycles(&empty[s], ph ^ 1, abort_flag, P.err)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sf = sSf + s * 3 * kMxSfBytes + kMxSfBytes;
+          if (GATEUP || !up)
+            tma_load_3d(sB + s * kMxBBytes + (up ? kMxBBytes / 2 : 0), m, &full[s], ks * kMxKStage, tile.n0, g);
+          if (GATEUP) {
+            bulk_load(sf + (up ? kMxSfBytes : 0), src + static_cast<size_t>(ks) * 512, kMxSfBytes, &full[s]);
+          } else if (up) {
+            bulk_load(sf, src + static_cast<size_t>(ks) * 512, kMxSfBytes, &full[s]);
+            if (two_b) bulk_load(sf + kMxSfBytes, src + static_cast<size_t>(kb + ks) * 512, kMxSfBytes, &full[s]);
+          }
+          if (++s == kMxStages) {
+            s = 0;
+            ph ^= 1;
+          }
         }
       }
-      if (!ok) break;
     }
   } else {
     // ----------------------------------------------------------- epilogue
@@ -524,7 +532,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
         }
       } else {
         // staged through the warp's buffer: whole-sector stores in row order
-        uint8_t* stg = sStg + (warp - 2) * kF4StgWarpBytes;
+        uint8_t* stg = sStg + (warp - 2) * kMxStgWarpBytes;
         const int rows_valid = tile.rows - quarter * 32;
         const size_t wrow = static_cast<size_t>(tile.row0 + quarter * 32);
 #pragma unroll
@@ -553,8 +561,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
               pk[i] = pack_bf16x2(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
             uint8_t* base =
                 reinterpret_cast<uint8_t*>(reinterpret_cast<__nv_bfloat16*>(pr.out) + wrow * pr.ldo + tile.n0 + j);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) store_rows_32B(stg, pk + 8 * q, lane, base + 32 * q, pr.ldo * 2, rows_valid);
+            store_rows_bf16x32(stg, pk, lane, reinterpret_cast<__nv_bfloat16*>(base), pr.ldo, rows_valid);
           }
         }
       }
