@@ -217,6 +217,13 @@ moe_status device_state(DeviceState** out) {
       if (cudaFuncSetAttribute(fp4_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kF4SmemBytes) !=
           cudaSuccess)
         return MOE_ERR_CUDA;
+      // the small kernel runs between large ones that take all of an SM's shared memory: with the same split of the L1
+      // array none of them waits for it to be changed
+      if (cudaFuncSetAttribute(few_prep_kernel<false>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared) != cudaSuccess ||
+          cudaFuncSetAttribute(few_prep_kernel<true>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+        return MOE_ERR_CUDA;
       if (cudaFuncSetAttribute(few_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                kFewMaxSmem - kFewStaticSmem) !=
               cudaSuccess ||
