@@ -1230,12 +1230,24 @@ moe_status enqueue_few_bf16(const moe_params* p, const Dims& d, const FewLayout&
   return MOE_OK;
 }
 
-// The workspace of an MXFP8 call: large enough for every smaller batch too, whichever form it takes.
+// The workspace of an MXFP8 call: large enough for every smaller batch too, whichever form it takes. All parts of the
+// layout grow with T but one: the router cuts its reduction into fewer splits for more tokens, so its partial logits
+// count with the largest size that any smaller batch gives them.
 size_t mx_workspace_bytes(const Dims& d) {
   Dims few = d;
   few.T = std::min(d.T, kFewMaxTokens);
-  const size_t small = few_fits(few) ? make_few_layout(few, true).total : make_mx_layout(few).total;
-  return few_fits(d) ? small : std::max(small, make_mx_layout(d).total);
+  size_t bytes = few_fits(few) ? make_few_layout(few, true).total : 0;
+  if (few_fits(d)) return bytes;
+  size_t most = 0;  // splits x tokens
+  const int tiles = (d.T + kRouterTokens - 1) / kRouterTokens;
+  for (int t = 1; t <= std::min(tiles, kSmCountHint); ++t) {  // one split from kSmCountHint tiles on
+    Dims part = d;
+    part.T = std::min(t * kRouterTokens, d.T);
+    most = std::max(most, static_cast<size_t>(router_splits(part)) * part.T);
+  }
+  const size_t own = static_cast<size_t>(router_splits(d)) * d.T;
+  auto partial = [&](size_t n) { return align_up(n * d.E * 4, kAlign); };
+  return std::max(bytes, make_mx_layout(d).total - partial(own) + partial(std::max(own, most)));
 }
 
 moe_status enqueue_few_mx(const moe_mxfp8_params* p, const Dims& d, const FewLayout& L, uint8_t* ws, DeviceState* s,
@@ -2235,11 +2247,11 @@ moe_status moe_block_forward_mxfp8(const moe_mxfp8_params* p, void* stream) {
   uint8_t* ws = nullptr;
   if (few_fits(d)) {
     const FewLayout L = make_few_layout(d, true);
-    MOE_TRY(call_workspace(p->workspace, p->workspace_bytes, L.total, s, st, &ws));
+    MOE_TRY(call_workspace(p->workspace, p->workspace_bytes, mx_workspace_bytes(d), s, st, &ws));
     return enqueue_few_mx(p, d, L, ws, s, st);
   }
   const MxLayout M = make_mx_layout(d);
-  MOE_TRY(call_workspace(p->workspace, p->workspace_bytes, M.total, s, st, &ws));
+  MOE_TRY(call_workspace(p->workspace, p->workspace_bytes, mx_workspace_bytes(d), s, st, &ws));
   return enqueue_block_mx(p, d, M, ws, s, st);
 }
 

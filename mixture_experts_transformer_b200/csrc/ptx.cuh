@@ -81,10 +81,8 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
-// mbar_wait with its limit taken from the SM's cycle counter. Reading
-// %globaltimer takes long enough (most of a microsecond) that a thread whose
-// barrier completes meanwhile notices late: the few-token kernel's chunk period
-// was 0.86 us with mbar_wait, whatever the chunk held.
+// mbar_wait with its limit taken from the SM's cycle counter, which a waiting
+// thread reads in a few cycles (%globaltimer is one counter of the whole GPU).
 constexpr long long kWaitTimeoutCycles = 4000000000ll;  // about 2 s at 1.9 GHz
 
 __device__ __forceinline__ bool mbar_wait_cycles(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err,

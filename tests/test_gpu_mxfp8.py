@@ -247,3 +247,61 @@ def test_block_against_oracle(dims, T, k, fed):
                               router_bias=None if bias is None else torch.from_numpy(bias).cuda())
     ok()
     check_block(w, xb, res, k, bias, xv)
+
+
+@pytest.mark.parametrize("T,k", [(1100, 4), (2000, 2)])
+def test_large_skewed_batches(T, k):
+    """Experts with many and with no rows (Zipf bias): a sample of tokens against the oracle, root mean square: the
+    routed outputs' bf16 storage alone (2^-8 of each at most) bounds it up to rare flipped codes of the GeGLU rows."""
+    w, dw = weights(SMALL), device_weights(SMALL)
+    mw = block.quantize_mxfp8(dw)
+    xb = inputs.make_x(T, SMALL.embed_dim, seed=T)
+    bias = 2 * inputs.zipf_router_bias(SMALL.num_experts)
+    buf = torch.full((T + 3, SMALL.embed_dim), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = block.mxfp8_workspace(mw, T, k)
+    res = block.forward_mxfp8(mw, block.bf16_tensor(xb), top_k=k, debug=True, out=buf[:T], workspace=ws,
+                              router_bias=torch.from_numpy(bias).cuda())
+    ok()
+    assert torch.all(buf[T:] == 7.0)
+    cnt = to_np(res.cnt)
+    assert cnt.sum() == T * k and cnt.max() > T // 2
+    tok = np.arange(0, T, 7)
+    idx, wts = to_np(res.idx)[tok], to_np(res.w)[tok]
+    out = mx.block(xb[tok], w.w_router, w.wg, w.wu, w.wd, w.sg, w.su, w.sd, k, routing=(idx, wts))
+    err = to_np(res.out_f32)[tok] - out
+    assert np.sqrt(np.mean(err**2)) <= 2.0**-8 * np.sqrt(np.mean(out**2))
+    again = block.forward_mxfp8(mw, block.bf16_tensor(xb), top_k=k, router_bias=torch.from_numpy(bias).cuda())
+    ok()
+    assert torch.equal(again.out, res.out)
+
+
+def test_large_batch_graph_and_refusals():
+    dw = device_weights(SMALL)
+    mw = block.quantize_mxfp8(dw)
+    T = 100
+    x = block.bf16_tensor(inputs.make_x(T, SMALL.embed_dim, seed=3))
+    ws = block.mxfp8_workspace(mw, T, 4)
+    ref = block.forward_mxfp8(mw, x, top_k=4, workspace=ws).out.clone()
+    out = torch.zeros_like(x)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        block.forward_mxfp8(mw, x, top_k=4, workspace=ws, out=out)
+    g.replay()
+    torch.cuda.synchronize()
+    ok()
+    assert torch.equal(out, ref)
+    del g
+    f = B.moe_block_forward_mxfp8
+    assert f(block.mxfp8_params(mw, T, x, out, top_k=4, workspace=ws[:-256])) == B.MOE_ERR_WORKSPACE
+    assert f(block.mxfp8_params(mw, T, x, out, top_k=4, workspace=ws[16:])) == B.MOE_ERR_ALIGNMENT
+    assert f(block.mxfp8_params(mw, T, x, x, top_k=4, workspace=ws)) == B.MOE_ERR_INVALID_ARG
+    q, sc = block.quantize_mxfp8_rows(x)
+    with pytest.raises(B.MoeError):
+        block.forward_mxfp8(mw, x, xq=q, top_k=4)
+    with pytest.raises(ValueError):
+        block.forward_mxfp8(mw, x, xq=q.float(), xs=sc, top_k=4)
+    with pytest.raises(ValueError):
+        block.forward_mxfp8(mw, x, xq=q, xs=sc[:, :-1], top_k=4)
+    ok()

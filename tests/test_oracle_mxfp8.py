@@ -175,3 +175,17 @@ def test_mxfp8_quantiser_refusals_and_sizes(lib):
     assert a(FAR, 2, 64, FAR, 3 * FAR, None) == bad
     assert B.moe_mxfp8_workspace_bytes(_mxp(E=12)) == 0
     assert B.moe_mxfp8_workspace_bytes(_mxp(T=64)) > B.moe_mxfp8_workspace_bytes(_mxp(T=0)) > 0
+
+
+@pytest.mark.parametrize("dims", [(2816, 128, 704, 2112), (8192, 128, 64, 64), (256, 16, 192, 320), (64, 8, 64, 64)])
+@pytest.mark.parametrize("k", [1, 8])
+def test_mxfp8_workspace_serves_smaller_batches(dims, k):
+    for T in list(range(40)) + list(range(100, 12000, 61)) + [896, 897, 900, 1025, 1153, 9476]:
+        p = B.MoeMxfp8Params()
+        p.T, p.top_k_experts = T, k
+        p.embed_dim, p.num_experts, p.expert_dim, p.hidden_dim = dims
+        sizes = [B.moe_mxfp8_workspace_bytes(p)]
+        for smaller in (max(0, T - 1), max(0, T - 61), T // 2, min(T, 16), min(T, 17)):
+            p.T = smaller
+            sizes.append(B.moe_mxfp8_workspace_bytes(p))
+        assert sizes[0] == max(sizes)
