@@ -433,6 +433,13 @@ class Mxfp8Linear:
     K: int
     N: int
 
+    def __post_init__(self):
+        sizes = B.moe_mxfp8_weight_bytes(self.groups, self.K, self.N)
+        for name, t, n in (("q", self.q, sizes[0]), ("sf", self.sf, sizes[1])):
+            if t.numel() != n or t.element_size() != 1 or not t.is_contiguous():
+                raise ValueError(f"{name}: {self.groups} Linears [{self.K}, {self.N}] need {n} contiguous bytes, got "
+                                 f"{tuple(t.shape)} {t.dtype}, strides {t.stride()}")
+
     def struct(self) -> B.MoeMxfp8Linear:
         return B.MoeMxfp8Linear(self.q.data_ptr(), self.sf.data_ptr())
 
@@ -470,6 +477,15 @@ class Mxfp8Weights:
     sg: Mxfp8Linear
     su: Mxfp8Linear
     sd: Mxfp8Linear
+
+    def __post_init__(self):
+        d = self.dims
+        for name, G, K, N in (("wg", d.num_experts, d.embed_dim, d.expert_dim), ("wu", d.num_experts, d.embed_dim, d.expert_dim),
+                              ("wd", d.num_experts, d.expert_dim, d.embed_dim), ("sg", 1, d.embed_dim, d.hidden_dim),
+                              ("su", 1, d.embed_dim, d.hidden_dim), ("sd", 1, d.hidden_dim, d.embed_dim)):
+            lin = getattr(self, name)
+            if (lin.groups, lin.K, lin.N) != (G, K, N):
+                raise ValueError(f"{name}: {G} Linears [{K}, {N}] expected, got {lin.groups} of [{lin.K}, {lin.N}]")
 
 
 def quantize_mxfp8(dw: DeviceWeights, stream=None) -> Mxfp8Weights:

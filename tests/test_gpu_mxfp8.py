@@ -305,3 +305,93 @@ def test_large_batch_graph_and_refusals():
     with pytest.raises(ValueError):
         block.forward_mxfp8(mw, x, xq=q, xs=sc[:, :-1], top_k=4)
     ok()
+
+
+# -------------------------------------------- offsets that pass 32 bits
+
+
+def test_rows_past_32_bit_offsets():
+    """2.2e9 elements: the rows behind the 2^31 and 2^32 byte and element borders equal the same rows alone."""
+    T, D = 134_500, 16384
+    assert T * D > 2**31
+    x = torch.empty((T, D), dtype=torch.bfloat16, device="cuda").normal_()
+    gamma = torch.empty(D, dtype=torch.bfloat16, device="cuda").uniform_(0.5, 1.5)
+    res = torch.empty_like(x).normal_()
+    big = block.add_rms_norm(x, gamma, residual=res, gamma_post=gamma, quantize=True)
+    qx, sx = block.quantize_mxfp8_rows(x)
+    ok()
+    for r in (0, 2**31 // D - 1, 2**31 // D, 2**30 // D, T - 3):
+        rows = slice(max(0, r - 1), r + 3)
+        one = block.add_rms_norm(x[rows].clone(), gamma, residual=res[rows].clone(), gamma_post=gamma, quantize=True)
+        for a, b in ((big.y, one.y), (big.sum, one.sum), (big.q, one.q), (big.scale, one.scale)):
+            assert torch.equal(a[rows].view(torch.uint8), b.view(torch.uint8))
+        q, s = block.quantize_mxfp8_rows(x[rows].clone())
+        assert torch.equal(qx[rows].view(torch.uint8), q.view(torch.uint8))
+        assert torch.equal(sx[rows].view(torch.uint8), s.view(torch.uint8))
+    ok()
+
+
+def test_batch_past_32_bit_offsets():
+    """70000 tokens of 4096 on all 8 experts: 560000 routed rows, 2.3e9 elements."""
+    dims = inputs.Dims(embed_dim=4096, num_experts=8, expert_dim=64, hidden_dim=64)
+    w, dw = weights(dims), device_weights(dims)
+    mw = block.quantize_mxfp8(dw)
+    T = 70_000
+    assert T * 8 * dims.embed_dim > 2**31
+    x = torch.empty((T, dims.embed_dim), dtype=torch.bfloat16, device="cuda").normal_()
+    res = block.forward_mxfp8(mw, x, top_k=8, debug=True)
+    ok()
+    tok = np.array([0, 1, 32767, 32768, 65535, 65536, T - 129, T - 1])
+    xb = to_np(x[torch.from_numpy(tok)].view(torch.int16)).view(np.uint16)
+    idx, wts = to_np(res.idx)[tok], to_np(res.w)[tok]
+    out = mx.block(xb, w.w_router, w.wg, w.wu, w.wd, w.sg, w.su, w.sd, 8, routing=(idx, wts))
+    err = to_np(res.out_f32)[tok] - out
+    # the routed outputs' bf16 storage (2^-9 rms each) and rare flipped codes, per token
+    assert np.all(np.sqrt(np.mean(err**2, -1)) <= 2.0**-8 * np.sqrt(np.mean(out**2, -1)))
+
+
+def test_weights_past_32_bit_offsets():
+    """128 experts of 4096 x 4160: 2.2e9 elements a matrix. The last eight equal the same eight alone, bit for bit:
+    quantised, and in both few-token forms and the grouped GEMMs."""
+    G, K, N, S = 128, 4096, 4160, 64
+    assert G * K * N > 2**31
+
+    def rand(*shape):
+        return torch.empty(shape, dtype=torch.bfloat16, device="cuda").normal_(0, 0.02)
+
+    big = block.DeviceWeights(inputs.Dims(K, G, N, S), rand(K, G), rand(G, K, N), rand(G, K, N), rand(G, N, K), rand(K, S),
+                              rand(K, S), rand(S, K))
+    last = block.DeviceWeights(inputs.Dims(K, 8, N, S), big.w_router[:, -8:].contiguous(), big.wg[-8:], big.wu[-8:],
+                               big.wd[-8:], big.sg, big.su, big.sd)
+    mbig, mlast = block.quantize_mxfp8(big), block.quantize_mxfp8(last)
+    ok()
+    assert torch.equal(mbig.wg.q[-8:].view(torch.uint8), mlast.wg.q.view(torch.uint8))
+    assert torch.equal(mbig.wd.q[-8:].view(torch.uint8), mlast.wd.q.view(torch.uint8))
+    n = mlast.wu.sf.numel()
+    assert torch.equal(mbig.wu.sf[-n:].view(torch.uint8), mlast.wu.sf.view(torch.uint8))
+    bias = torch.full((G,), -1e30, device="cuda")
+    bias[-8:] = 0
+    for T in (1, 9, 20):
+        x = torch.empty((T, K), dtype=torch.bfloat16, device="cuda").normal_()
+        if T <= 16:
+            a = block.forward_few(big, x, top_k=2, router_bias=bias, debug=True)
+            b = block.forward_few(last, x, top_k=2, debug=True)
+            assert torch.equal(a.idx - (G - 8), b.idx) and torch.equal(a.out_f32, b.out_f32)
+        a = block.forward_mxfp8(mbig, x, top_k=2, router_bias=bias, debug=True)
+        b = block.forward_mxfp8(mlast, x, top_k=2, debug=True)
+        ok()
+        assert torch.equal(a.idx - (G - 8), b.idx) and torch.equal(a.out_f32, b.out_f32)
+        assert torch.isfinite(a.out_f32).all()
+
+
+def test_more_choices_than_the_few_token_form_holds():
+    """top_k 40: one token takes the grouped GEMMs."""
+    dims = inputs.Dims(embed_dim=128, num_experts=64, expert_dim=64, hidden_dim=64)
+    w, dw = weights(dims), device_weights(dims)
+    mw = block.quantize_mxfp8(dw)
+    for T in (1, 16, 33):
+        xb = inputs.make_x(T, 128, seed=T)
+        res = block.forward_mxfp8(mw, block.bf16_tensor(xb), top_k=40, debug=True)
+        ok()
+        assert B.moe_last_launch_count() > 2
+        check_block(w, xb, res, 40)

@@ -9,6 +9,7 @@ import pytest
 import torch
 
 from mixture_experts_transformer_b200 import binding as B
+from mixture_experts_transformer_b200 import block
 from mixture_experts_transformer_b200 import build as mbuild
 from mixture_experts_transformer_b200 import inputs
 from oracle import moe_oracle as mo
@@ -189,3 +190,23 @@ def test_mxfp8_workspace_serves_smaller_batches(dims, k):
             p.T = smaller
             sizes.append(B.moe_mxfp8_workspace_bytes(p))
         assert sizes[0] == max(sizes)
+
+
+def test_mxfp8_weights_of_other_sizes_are_refused(lib):
+    def linear(G, K, N, cut=0, dtype=torch.uint8):
+        qb, sfb = B.moe_mxfp8_weight_bytes(G, K, N)
+        return block.Mxfp8Linear(torch.empty(qb - cut, dtype=dtype), torch.empty(sfb, dtype=torch.uint8), G, K, N)
+
+    d = SMALL
+    gu, dn = (d.num_experts, d.embed_dim, d.expert_dim), (d.num_experts, d.expert_dim, d.embed_dim)
+    sgu, sdn = (1, d.embed_dim, d.hidden_dim), (1, d.hidden_dim, d.embed_dim)
+    router = torch.empty((d.embed_dim, d.num_experts), dtype=torch.bfloat16)
+    block.Mxfp8Weights(d, router, linear(*gu), linear(*gu), linear(*dn), linear(*sgu), linear(*sgu), linear(*sdn))
+    with pytest.raises(ValueError, match="contiguous bytes"):
+        linear(*gu, cut=1)
+    with pytest.raises(ValueError, match="contiguous bytes"):
+        linear(*gu, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="wd: 8 Linears"):
+        block.Mxfp8Weights(d, router, linear(*gu), linear(*gu), linear(*gu), linear(*sgu), linear(*sgu), linear(*sdn))
+    with pytest.raises(ValueError, match="wu: 8 Linears"):
+        block.Mxfp8Weights(d, router, linear(*gu), linear(7, *gu[1:]), linear(*dn), linear(*sgu), linear(*sgu), linear(*sdn))
