@@ -203,12 +203,6 @@ __host__ __device__ constexpr uint32_t few_idesc_bf16(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(128 >> 4) << 24);
 }
-// The two words of an sdesc_sw128 descriptor: only the low one moves with the address (+ bytes / 16), so the MMA thread
-// adds to it instead of building 64-bit descriptors - its instruction stream is what a chunk waits for otherwise (16
-// MMAs with built descriptors took 0.6 us to issue, and a chunk 0.86 us).
-__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
-__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
-
 __device__ __forceinline__ void few_umma_bf16(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi,
                                               uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -220,18 +214,6 @@ __device__ __forceinline__ void few_umma_bf16(uint32_t d, uint32_t alo, uint32_t
       "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void few_umma_mxf8(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi,
-                                              uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "mov.b64 a, {%1, %2};\n\t"
-      "mov.b64 b, {%3, %4};\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.block32 [%0], a, b, %5, [%7], [%8], p;\n\t}" ::"r"(d),
-      "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
-      : "memory");
-}
-
 // fp32 as an unsigned integer of the same order (a positive NaN above infinity)
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t b = __float_as_uint(v);
@@ -625,9 +607,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (j == 2 && k_left <= 64) break;
-          few_umma_mxf8(d, al + j * 2, desc_hi(1024), bl + j * 2, desc_hi(1024), idesc_mxf8_m128(16, j), sf, sf + 8,
+          umma_mxf8(d, al + j * 2, desc_hi(1024), bl + j * 2, desc_hi(1024), idesc_mxf8_m128(16, j), sf, sf + 8,
                         !first || j != 0);
-          few_umma_mxf8(d + n, al + kFewWBytes / 32 + j * 2, desc_hi(1024), bl + j * 2, desc_hi(1024),
+          umma_mxf8(d + n, al + kFewWBytes / 32 + j * 2, desc_hi(1024), bl + j * 2, desc_hi(1024),
                         idesc_mxf8_m128(16, j), sf + 4, sf + 8, !first || j != 0);
         }
       };

@@ -395,3 +395,24 @@ def test_more_choices_than_the_few_token_form_holds():
         ok()
         assert B.moe_last_launch_count() > 2
         check_block(w, xb, res, 40)
+
+
+@pytest.mark.parametrize("D,F,S", [(256, 192, 320), (320, 64, 448), (64, 64, 64), (192, 128, 256)])
+@pytest.mark.parametrize("T,k", [(160, 8), (257, 8), (700, 3)])
+@pytest.mark.parametrize("fed", [False, True])
+def test_block_of_many_rows_per_expert(D, F, S, T, k, fed):
+    """Experts with 160 routed rows and more on average, some with few or none (SM pairs)."""
+    dims = inputs.Dims(D, 8, F, S)
+    w, dw = weights(dims), device_weights(dims)
+    mw = block.quantize_mxfp8(dw)
+    xb = inputs.make_x(T, D, seed=T)
+    xq = xs = xv = bias = None
+    if fed:
+        xq, xs = block.quantize_mxfp8_rows(block.bf16_tensor(inputs.make_x(T, D, seed=T + 1)))
+        xv = dequant(xq, xs)
+    if k < 8:
+        bias = 2 * inputs.zipf_router_bias(8)
+    res = block.forward_mxfp8(mw, block.bf16_tensor(xb), xq=xq, xs=xs, top_k=k, debug=True,
+                              router_bias=None if bias is None else torch.from_numpy(bias).cuda())
+    ok()
+    check_block(w, xb, res, k, bias, xv)
