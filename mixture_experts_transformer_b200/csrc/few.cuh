@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   int* sCount = const_cast<int*>(abort_flag) + 1;  // touched experts
   int* sLast = sCount + 1;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int cta = blockIdx.x, grid = gridDim.x;
   const int nr = (D + kFewRouterRows - 1) / kFewRouterRows;  // parts of the logits
   const int ks_dn = (P.S + kKC - 1) / kKC, ke_dn = (P.F + kKC - 1) / kKC;
@@ -574,59 +574,59 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   const uint32_t tmem = *tmem_slot;
 
   if (warp == kFewMmaWarp) {
-    // ------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 0, hph = 0, q = 0;  // q: accumulators used so far
-      bool ok = true, any = false;
-      const uint32_t xhi = desc_hi(rows == 8 ? 0 : 1024);
-      auto begin_acc = [&]() -> uint32_t {  // the accumulator's first TMEM column
-        if (ok && !mbar_wait_cycles(&acc_empty[q & 1], ((q >> 1) & 1) ^ 1, abort_flag, P.err)) ok = false;
-        tc_fence_after_sync();
-        return tmem + (q & 1) * kFewTmemAcc;
-      };
-      auto end_acc = [&]() {
-        if (ok) umma_commit(&acc_full[q & 1]);
-        ++q;
-      };
-      auto end_chunk = [&]() {
-        any = true;
-        umma_commit(&empty[s]);
-        if (++s == P.stages) {
-          s = 0;
-          ph ^= 1;
-        }
-      };
-      // MXFP8: both M = 128 tiles of a chunk (accumulators d and d + n) over the K it has left (64: half a chunk)
-      auto mma_mx = [&](uint32_t d, int n, uint32_t a, uint32_t b, bool first, int k_left) {
-        const uint32_t sf = tmem + kFewTmemSf + s * 16;
-        tmem_cp_scales(sf, a + kFewWBytes);
-        tmem_cp_scales(sf + 4, a + kFewWBytes + 512);
-        tmem_cp_scales(sf + 8, b + 16 * 128);
-        const uint32_t al = desc_lo(a, 16), bl = desc_lo(b, 16);
+    // ------------------------------------------------------- MMA issuer: the whole warp walks, one lane issues
+    int s = 0;
+    uint32_t ph = 0, hph = 0, q = 0;  // q: accumulators used so far
+    bool ok = true, any = false;
+    const uint32_t xhi = desc_hi(rows == 8 ? 0 : 1024);
+    auto begin_acc = [&]() -> uint32_t {  // the accumulator's first TMEM column
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_cycles(&acc_empty[q & 1], ((q >> 1) & 1) ^ 1, abort_flag, P.err));
+      tc_fence_after_sync();
+      return tmem + (q & 1) * kFewTmemAcc;
+    };
+    auto end_acc = [&]() {
+      if (ok && elect_one()) umma_commit(&acc_full[q & 1]);
+      ++q;
+    };
+    auto end_chunk = [&]() {
+      __syncwarp();
+      any = true;
+      if (++s == P.stages) {
+        s = 0;
+        ph ^= 1;
+      }
+    };
+    // MXFP8: both M = 128 tiles of a chunk (accumulators d and d + n) over the K it has left (64: half a chunk)
+    auto mma_mx = [&](uint32_t d, int n, uint32_t a, uint32_t b, bool first, int k_left) {
+      const uint32_t sf = tmem + kFewTmemSf + s * 16;
+      tmem_cp_scales(sf, a + kFewWBytes);
+      tmem_cp_scales(sf + 4, a + kFewWBytes + 512);
+      tmem_cp_scales(sf + 8, b + 16 * 128);
+      const uint32_t al = desc_lo(a, 16), bl = desc_lo(b, 16);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (j == 2 && k_left <= 64) break;
-          umma_mxf8(d, al + j * 2, desc_hi(1024), bl + j * 2, desc_hi(1024), idesc_mxf8_m128(16, j), sf, sf + 8,
-                        !first || j != 0);
-          umma_mxf8(d + n, al + kFewWBytes / 32 + j * 2, desc_hi(1024), bl + j * 2, desc_hi(1024),
-                        idesc_mxf8_m128(16, j), sf + 4, sf + 8, !first || j != 0);
-        }
-      };
-      // a phase of gate|up chunks
-      auto run_gu = [&](const int* begin) {
-        const int i1 = begin[cta + 1];
-        for (int i = begin[cta]; ok && i < i1;) {
-          const int iend = min(i1, (i / ck + 1) * ck);
-          const uint32_t d = begin_acc();
-          int kc = i % ck;
-          for (bool first = true; ok && i < iend; ++i, ++kc, first = false) {
-            if (!mbar_wait_cycles(&full[s], ph, abort_flag, P.err)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after_sync();
-            const uint32_t a = smem_u32(ring + s * stage_bytes), b = a + kHOff;
+      for (int j = 0; j < 4; ++j) {
+        if (j == 2 && k_left <= 64) break;
+        umma_mxf8(d, al + j * 2, desc_hi(1024), bl + j * 2, desc_hi(1024), idesc_mxf8_m128(16, j), sf, sf + 8,
+                  !first || j != 0);
+        umma_mxf8(d + n, al + kFewWBytes / 32 + j * 2, desc_hi(1024), bl + j * 2, desc_hi(1024),
+                  idesc_mxf8_m128(16, j), sf + 4, sf + 8, !first || j != 0);
+      }
+    };
+    // a phase of gate|up chunks
+    auto run_gu = [&](const int* begin) {
+      const int i1 = warp_uniform(begin[cta + 1]);
+      for (int i = warp_uniform(begin[cta]); ok && i < i1;) {
+        const int iend = min(i1, (i / ck + 1) * ck);
+        const uint32_t d = begin_acc();
+        int kc = i % ck;
+        for (bool first = true; ok && i < iend; ++i, ++kc, first = false) {
+          if (!__all_sync(0xffffffffu, mbar_wait_cycles(&full[s], ph, abort_flag, P.err))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t a = smem_u32(ring + s * stage_bytes), b = a + kHOff;
+          if (elect_one()) {
             if constexpr (MX) {
               mma_mx(d, 16, a, b, first, D - kc * 128);
             } else {
@@ -638,35 +638,38 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                               !first || j != 0);
               }
             }
-            end_chunk();
+            umma_commit(&empty[s]);
           }
-          end_acc();
+          end_chunk();
         }
-      };
-      run_gu(sBegS);
-      if (ok && !mbar_wait_cycles(routed, 0, abort_flag, P.err)) ok = false;
-      if (ok) {
-        const int nact = *sCount;
-        run_gu(sBegE);
-        const int len = ks_dn + nact * ke_dn;
-        const int i1 = sBegD[cta + 1];
-        for (int i = sBegD[cta]; ok && i < i1;) {  // one accumulator per run of chunks of one source
-          const int u = i / len;
-          int kc = i - u * len;
-          const int run_end = kc < ks_dn ? ks_dn : ks_dn + ((kc - ks_dn) / ke_dn + 1) * ke_dn;
-          const int iend = min(i1, u * len + run_end);
-          const int run0 = kc < ks_dn ? 0 : run_end - ke_dn;
-          const int K = kc < ks_dn ? P.S : P.F;
-          const uint32_t d = begin_acc();
-          for (bool first = true; ok && i < iend; ++i, ++kc, first = false) {
-            if (!mbar_wait_cycles(&full[s], ph, abort_flag, P.err) ||
-                !mbar_wait_cycles(&hfull[s], (hph >> s) & 1u, abort_flag, P.err)) {
-              ok = false;
-              break;
-            }
-            hph ^= 1u << s;
-            tc_fence_after_sync();
-            const uint32_t a = smem_u32(ring + s * stage_bytes), b = a + kHOff;
+        end_acc();
+      }
+    };
+    run_gu(sBegS);
+    ok = ok && __all_sync(0xffffffffu, mbar_wait_cycles(routed, 0, abort_flag, P.err));
+    if (ok) {
+      const int nact = warp_uniform(*sCount);
+      run_gu(sBegE);
+      const int len = ks_dn + nact * ke_dn;
+      const int i1 = warp_uniform(sBegD[cta + 1]);
+      for (int i = warp_uniform(sBegD[cta]); ok && i < i1;) {  // one accumulator per run of chunks of one source
+        const int u = i / len;
+        int kc = i - u * len;
+        const int run_end = kc < ks_dn ? ks_dn : ks_dn + ((kc - ks_dn) / ke_dn + 1) * ke_dn;
+        const int iend = min(i1, u * len + run_end);
+        const int run0 = kc < ks_dn ? 0 : run_end - ke_dn;
+        const int K = kc < ks_dn ? P.S : P.F;
+        const uint32_t d = begin_acc();
+        for (bool first = true; ok && i < iend; ++i, ++kc, first = false) {
+          if (!__all_sync(0xffffffffu, mbar_wait_cycles(&full[s], ph, abort_flag, P.err) &&
+                                           mbar_wait_cycles(&hfull[s], (hph >> s) & 1u, abort_flag, P.err))) {
+            ok = false;
+            break;
+          }
+          hph ^= 1u << s;
+          tc_fence_after_sync();
+          const uint32_t a = smem_u32(ring + s * stage_bytes), b = a + kHOff;
+          if (elect_one()) {
             if constexpr (MX) {
               mma_mx(d, 16, a, b, first, K - (kc - run0) * 128);
             } else {
@@ -679,16 +682,17 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                               !first || j != 0);
               }
             }
-            end_chunk();
+            umma_commit(&empty[s]);
           }
-          end_acc();
+          end_chunk();
         }
+        end_acc();
       }
-      if (any) {
-        umma_commit(drain);
-        uint32_t dummy = 0;
-        mbar_wait_cycles(drain, 0, reinterpret_cast<volatile int*>(&dummy), P.err);
-      }
+    }
+    if (any && elect_one()) {
+      umma_commit(drain);
+      uint32_t dummy = 0;
+      mbar_wait_cycles(drain, 0, reinterpret_cast<volatile int*>(&dummy), P.err);
     }
     __syncwarp();
     bar_named(4, 32 * (kFewConsWarps + 1));  // the consumers have read their last accumulator

@@ -152,7 +152,6 @@ struct DeviceState {
   void* ws = nullptr;
   size_t ws_bytes = 0;
   int pair_clusters_dn = 0;  // SM-pair clusters of the pair down GEMM that fit on the device at once
-  int pair_clusters_mx = 0;  // of the MXFP8 GEMMs
 };
 DeviceState g_dev[kMaxDevices];
 
@@ -237,19 +236,6 @@ moe_status device_state(DeviceState** out) {
           cudaFuncSetAttribute(mx_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmemBytes) !=
               cudaSuccess)
         return MOE_ERR_CUDA;
-      if (cudaFuncSetAttribute(mx_gemm_pair_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxPSmemBytes) !=
-              cudaSuccess ||
-          cudaFuncSetAttribute(mx_gemm_pair_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               kMxPSmemBytes) != cudaSuccess)
-        return MOE_ERR_CUDA;
-      {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2 * (s.sm_count / 2));
-        cfg.blockDim = dim3(kMxPThreads);
-        cfg.dynamicSmemBytes = kMxPSmemBytes;
-        if (cudaOccupancyMaxActiveClusters(&s.pair_clusters_mx, mx_gemm_pair_kernel<true>, &cfg) != cudaSuccess)
-          return MOE_ERR_CUDA;
-      }
     }
     s.init = true;
   }
@@ -1024,33 +1010,6 @@ moe_status check_mx_args(const moe_mxfp8_params* p, Dims* d) {
   return MOE_OK;
 }
 
-// Scale tiles as rows of 128 words, one row per copy.
-bool map_sf(CUtensorMap* m, const void* base, uint64_t tiles) {
-  const cuuint64_t dims[2] = {128, tiles};
-  const cuuint64_t strides[1] = {512};
-  const cuuint32_t box[2] = {128, 1};
-  const cuuint32_t estr[2] = {1, 1};
-  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Large batches run the MXFP8 GEMMs on SM pairs.
-bool mx_pairs(const Dims& d, const DeviceState* s) {
-  return static_cast<long long>(d.T) * d.k >= 160LL * d.E && s->pair_clusters_mx > 0;
-}
-
-// One problem of a paired GEMM; b1 / up: the up weights (gate|up).
-bool mx_pair_problem(MxPairParams* P, int i, const MxProblem& pr, const void* a, uint64_t rows, const uint8_t* b0,
-                     const uint8_t* b1) {
-  const uint64_t kb = mx_kblocks(pr.K), nb = static_cast<uint64_t>((pr.N + 127) / 128) * kb * pr.groups;
-  P->prob[i] = pr;
-  return map_2d_u8(&P->tmA[i], a, rows, pr.K) && map_2d_u8(&P->tmAm[i], a, rows, pr.K, kMxAMidRows) &&
-         map_2d_u8(&P->tmAs[i], a, rows, pr.K, kMxASmallRows) && map_3d_u8(&P->tmB0[i], b0, pr.groups, pr.N, pr.K) &&
-         (!b1 || map_3d_u8(&P->tmB1[i], b1, pr.groups, pr.N, pr.K)) && map_sf(&P->tmSa[i], pr.sfa, pr.a_rows / 128 * kb) &&
-         map_sf(&P->tmSb0[i], pr.sfb0, nb) && (!b1 || map_sf(&P->tmSb1[i], pr.sfb1, nb));
-}
-
 moe_status enqueue_block_mx(const moe_mxfp8_params* p, const Dims& d, const MxLayout& M, uint8_t* ws, DeviceState* s,
                             cudaStream_t st) {
   const Layout& L = M.r;
@@ -1063,14 +1022,13 @@ moe_status enqueue_block_mx(const moe_mxfp8_params* p, const Dims& d, const MxLa
   int32_t* base = reinterpret_cast<int32_t*>(ws + L.base);
   TileCounts* counts = reinterpret_cast<TileCounts*>(ws + L.counts);
   const int rp = static_cast<int>(M.r_pad), tp = static_cast<int>(M.t_pad);
-  const int pairs = mx_pairs(d, s) ? 1 : 0;
 
   MOE_TRY(enqueue_route(d, L, ws, p->x, p->w_router, p->router_bias, idx, w, st));
   {
     LaunchScope ls_(kKRouteScan, st);
     MOE_TRY(ls_.done(launch_k(route_scan_kernel, kScanCtas, kScanThreads, 0, st, masks, L.nchunks, d.T, d.E, d.F, d.S,
                               d.D, base, cnt, off, reinterpret_cast<Tile*>(ws + L.tiles_gu),
-                              reinterpret_cast<Tile*>(ws + L.tiles_dn), counts, 1, 256, 128, pairs, pairs, 0, d.E)));
+                              reinterpret_cast<Tile*>(ws + L.tiles_dn), counts, 1, 256, 128, 0, 0, 0, d.E)));
   }
   {
     const int blocks = static_cast<int>(std::min<long long>((d.T + 7LL) / 8, 148LL * 64));  // a warp per token
@@ -1089,70 +1047,47 @@ moe_status enqueue_block_mx(const moe_mxfp8_params* p, const Dims& d, const MxLa
   const MxProblem gu1{d.D, d.S, 1, tp, ws + M.xsf_tok, p->sg.sf, p->su.sf, ws + M.hsq, ws + M.hssf, d.S, 0};
   const MxProblem dn0{d.F, d.D, d.E, rp, ws + M.hsf, p->wd.sf, p->wd.sf, ws + M.y, nullptr, d.D, 0};
   const MxProblem dn1{d.S, d.D, 1, tp, ws + M.hssf, p->sd.sf, p->sd.sf, sbuf, nullptr, d.D, 1};
-  if (pairs) {
-    MxPairParams G;
-    std::memset(&G, 0, sizeof(G));
-    if (!mx_pair_problem(&G, 0, gu0, ws + M.xq_perm, rp, p->wg.q, p->wu.q) ||
-        !mx_pair_problem(&G, 1, gu1, xtok, d.T, p->sg.q, p->su.q))
-      return MOE_ERR_CUDA;
-    G.nprob = 2;
-    G.tiles = reinterpret_cast<const Tile*>(ws + L.tiles_gu);
-    G.num_tiles = &counts->gateup;
-    G.err = s->err;
-    {
-      LaunchScope ls_(kKMxGateUp, st);
-      MOE_TRY(ls_.done(launch_k(mx_gemm_pair_kernel<true>, 2 * s->pair_clusters_mx, kMxPThreads, kMxPSmemBytes, st, G)));
-    }
-    if (!mx_pair_problem(&G, 0, dn0, ws + M.hq, rp, p->wd.q, nullptr) ||
-        !mx_pair_problem(&G, 1, dn1, ws + M.hsq, tp, p->sd.q, nullptr))
-      return MOE_ERR_CUDA;
-    G.tiles = reinterpret_cast<const Tile*>(ws + L.tiles_dn);
-    G.num_tiles = &counts->down;
-    LaunchScope ls_(kKMxDown, st);
-    MOE_TRY(ls_.done(launch_k(mx_gemm_pair_kernel<false>, 2 * s->pair_clusters_mx, kMxPThreads, kMxPSmemBytes, st, G)));
-  } else {
-    MxParams gu;
-    std::memset(&gu, 0, sizeof(gu));
-    if (!map_2d_u8(&gu.tmA[0], ws + M.xq_perm, rp, d.D) || !map_2d_u8(&gu.tmAs[0], ws + M.xq_perm, rp, d.D, kMxASmallRows) ||
-        !map_2d_u8(&gu.tmAm[0], ws + M.xq_perm, rp, d.D, kMxAMidRows) ||
-        !map_2d_u8(&gu.tmAm[1], xtok, d.T, d.D, kMxAMidRows) ||
-        !map_3d_u8(&gu.tmB0[0], p->wg.q, d.E, d.F, d.D) || !map_3d_u8(&gu.tmB1[0], p->wu.q, d.E, d.F, d.D) ||
-        !map_2d_u8(&gu.tmA[1], xtok, d.T, d.D) || !map_2d_u8(&gu.tmAs[1], xtok, d.T, d.D, kMxASmallRows) ||
-        !map_3d_u8(&gu.tmB0[1], p->sg.q, 1, d.S, d.D) || !map_3d_u8(&gu.tmB1[1], p->su.q, 1, d.S, d.D))
-      return MOE_ERR_CUDA;
-    gu.prob[0] = gu0;
-    gu.prob[1] = gu1;
-    gu.nprob = 2;
-    gu.tiles = reinterpret_cast<const Tile*>(ws + L.tiles_gu);
-    gu.num_tiles = &counts->gateup;
-    gu.next_tile = &counts->next_gateup;
-    gu.err = s->err;
-    {
-      LaunchScope ls_(kKMxGateUp, st);
-      const int grid = std::min(s->sm_count, L.max_tiles_gu);
-      MOE_TRY(ls_.done(launch_k(mx_gemm_kernel<true>, grid, kMxThreads, kMxSmemBytes, st, gu)));
-    }
+  MxParams gu;
+  std::memset(&gu, 0, sizeof(gu));
+  if (!map_2d_u8(&gu.tmA[0], ws + M.xq_perm, rp, d.D) || !map_2d_u8(&gu.tmAs[0], ws + M.xq_perm, rp, d.D, kMxASmallRows) ||
+      !map_2d_u8(&gu.tmAm[0], ws + M.xq_perm, rp, d.D, kMxAMidRows) ||
+      !map_2d_u8(&gu.tmAm[1], xtok, d.T, d.D, kMxAMidRows) ||
+      !map_3d_u8(&gu.tmB0[0], p->wg.q, d.E, d.F, d.D) || !map_3d_u8(&gu.tmB1[0], p->wu.q, d.E, d.F, d.D) ||
+      !map_2d_u8(&gu.tmA[1], xtok, d.T, d.D) || !map_2d_u8(&gu.tmAs[1], xtok, d.T, d.D, kMxASmallRows) ||
+      !map_3d_u8(&gu.tmB0[1], p->sg.q, 1, d.S, d.D) || !map_3d_u8(&gu.tmB1[1], p->su.q, 1, d.S, d.D))
+    return MOE_ERR_CUDA;
+  gu.prob[0] = gu0;
+  gu.prob[1] = gu1;
+  gu.nprob = 2;
+  gu.tiles = reinterpret_cast<const Tile*>(ws + L.tiles_gu);
+  gu.num_tiles = &counts->gateup;
+  gu.next_tile = &counts->next_gateup;
+  gu.err = s->err;
+  {
+    LaunchScope ls_(kKMxGateUp, st);
+    const int grid = std::min(s->sm_count, L.max_tiles_gu);
+    MOE_TRY(ls_.done(launch_k(mx_gemm_kernel<true>, grid, kMxThreads, kMxSmemBytes, st, gu)));
+  }
 
-    MxParams dn;
-    std::memset(&dn, 0, sizeof(dn));
-    if (!map_2d_u8(&dn.tmAm[0], ws + M.hq, rp, d.F, kMxAMidRows) || !map_2d_u8(&dn.tmAm[1], ws + M.hsq, tp, d.S, kMxAMidRows) ||
-        !map_2d_u8(&dn.tmA[0], ws + M.hq, rp, d.F) || !map_2d_u8(&dn.tmAs[0], ws + M.hq, rp, d.F, kMxASmallRows) ||
-        !map_2d_u8(&dn.tmA[1], ws + M.hsq, tp, d.S) || !map_2d_u8(&dn.tmAs[1], ws + M.hsq, tp, d.S, kMxASmallRows) ||
-        !map_3d_u8(&dn.tmB0[0], p->wd.q, d.E, d.D, d.F) || !map_3d_u8(&dn.tmB0[1], p->sd.q, 1, d.D, d.S) ||
-        !map_3d_u8(&dn.tmBw[0], p->wd.q, d.E, d.D, d.F, 256) || !map_3d_u8(&dn.tmBw[1], p->sd.q, 1, d.D, d.S, 256))
-      return MOE_ERR_CUDA;
-    dn.prob[0] = dn0;
-    dn.prob[1] = dn1;
-    dn.nprob = 2;
-    dn.tiles = reinterpret_cast<const Tile*>(ws + L.tiles_dn);
-    dn.num_tiles = &counts->down;
-    dn.next_tile = &counts->next_down;
-    dn.err = s->err;
-    {
-      LaunchScope ls_(kKMxDown, st);
-      const int grid = std::min(s->sm_count, L.max_tiles_dn);
-      MOE_TRY(ls_.done(launch_k(mx_gemm_kernel<false>, grid, kMxThreads, kMxSmemBytes, st, dn)));
-    }
+  MxParams dn;
+  std::memset(&dn, 0, sizeof(dn));
+  if (!map_2d_u8(&dn.tmAm[0], ws + M.hq, rp, d.F, kMxAMidRows) || !map_2d_u8(&dn.tmAm[1], ws + M.hsq, tp, d.S, kMxAMidRows) ||
+      !map_2d_u8(&dn.tmA[0], ws + M.hq, rp, d.F) || !map_2d_u8(&dn.tmAs[0], ws + M.hq, rp, d.F, kMxASmallRows) ||
+      !map_2d_u8(&dn.tmA[1], ws + M.hsq, tp, d.S) || !map_2d_u8(&dn.tmAs[1], ws + M.hsq, tp, d.S, kMxASmallRows) ||
+      !map_3d_u8(&dn.tmB0[0], p->wd.q, d.E, d.D, d.F) || !map_3d_u8(&dn.tmB0[1], p->sd.q, 1, d.D, d.S) ||
+      !map_3d_u8(&dn.tmBw[0], p->wd.q, d.E, d.D, d.F, 256) || !map_3d_u8(&dn.tmBw[1], p->sd.q, 1, d.D, d.S, 256))
+    return MOE_ERR_CUDA;
+  dn.prob[0] = dn0;
+  dn.prob[1] = dn1;
+  dn.nprob = 2;
+  dn.tiles = reinterpret_cast<const Tile*>(ws + L.tiles_dn);
+  dn.num_tiles = &counts->down;
+  dn.next_tile = &counts->next_down;
+  dn.err = s->err;
+  {
+    LaunchScope ls_(kKMxDown, st);
+    const int grid = std::min(s->sm_count, L.max_tiles_dn);
+    MOE_TRY(ls_.done(launch_k(mx_gemm_kernel<false>, grid, kMxThreads, kMxSmemBytes, st, dn)));
   }
   {
     LaunchScope ls_(kKCombine, st);

@@ -19,7 +19,6 @@
 #pragma once
 
 #include "grouped_gemm.cuh"
-#include "grouped_gemm_pair.cuh"
 #include "mxformat.cuh"
 #include "nvfp4.cuh"
 #include "ptx.cuh"
@@ -244,6 +243,52 @@ __device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t saddr) {
       : "memory");
 }
 
+// What an epilogue warp does with its 32 rows (rows_valid of them, from row on) of a tile's accumulator, a row a thread:
+// GeGLU and MXFP8 codes, or output rows through the warp's staging buffer (whole-sector stores in row order).
+template <bool GATEUP>
+__device__ __forceinline__ void mx_epilogue(const MxProblem& pr, uint32_t (&acc)[4][32], int rows_valid, int row, int n0,
+                                            int wn, int half, int lane, uint8_t* stg) {
+  if (rows_valid <= 0) return;
+  if constexpr (GATEUP) {
+    const int kbo = mx_kblocks(pr.N);
+    uint8_t* q = reinterpret_cast<uint8_t*>(pr.out) + static_cast<size_t>(row + lane) * pr.N + n0;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int j = half * 32 + 64 * c;
+      if (j >= wn) continue;
+      float v[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        v[i] = gelu_tanh_exact(__uint_as_float(acc[2 * c][i])) * __uint_as_float(acc[2 * c + 1][i]);
+      uint4 codes[2];
+      const uint32_t sc = mx_group(v, codes);
+      if (lane < rows_valid) {
+        reinterpret_cast<uint4*>(q + j)[0] = codes[0];
+        reinterpret_cast<uint4*>(q + j)[1] = codes[1];
+        pr.out_sf[mx_sf_offset(row + lane, (n0 + j) / 32, kbo)] = static_cast<uint8_t>(sc);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int j = half * 32 + 64 * c;
+      if (j >= wn) continue;
+      uint32_t* a = acc[c];
+      const size_t at = static_cast<size_t>(row) * pr.ldo + n0 + j;
+      if (pr.out_f32) {
+        uint8_t* base = reinterpret_cast<uint8_t*>(reinterpret_cast<float*>(pr.out) + at);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) store_rows_32B(stg, a + 8 * q, lane, base + 32 * q, pr.ldo * 4, rows_valid);
+      } else {
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
+        store_rows_bf16x32(stg, pk, lane, reinterpret_cast<__nv_bfloat16*>(pr.out) + at, pr.ldo, rows_valid);
+      }
+    }
+  }
+}
+
 // TMEM columns [0, 256): the accumulator (GATEUP: gate 0..127, up 128..255;
 // DOWN: output columns n0 .. n0+255); from 256: one scale slot per stage, A
 // scales at +0, B block 0 at +4, B block 1 at +8.
@@ -273,7 +318,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
   uint64_t* tile_empty = tile_full + kTileRing;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tile_empty + kTileRing);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* tile_ring = abort_flag + 1;
+  int4* tile_ring = reinterpret_cast<int4*>((reinterpret_cast<uintptr_t>(tmem_slot + 2) + 15) & ~uintptr_t(15));
 
   const int warp = warp_uniform(threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -310,24 +355,24 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
   const uint32_t tmem_base = *tmem_slot;
   pdl_wait_then_release();
   const int num_tiles = *P.num_tiles;
-  // Tile indices: the producer takes them from the work counter and publishes
-  // them in the ring (-1 ends the work), the other roles read them in order.
+  // Tiles: the producer takes their indices from the work counter and publishes the tiles in the ring (pg, row0, rows,
+  // n0; pg -1 ends the work), the other roles read them in order.
   int rs = 0;
   uint32_t rph = 0;
-  auto next_tile = [&](bool whole_warp) -> int {
-    int ti = -1;
+  auto next_tile = [&](bool whole_warp) -> Tile {
+    int4 v = make_int4(-1, 0, 0, 0);
     if (lane == 0) {
       if (mbar_wait_cycles(&tile_full[rs], rph, abort_flag, P.err)) {
-        ti = tile_ring[rs];
+        v = tile_ring[rs];
         mbar_arrive(&tile_empty[rs]);
       }
     }
-    if (whole_warp) ti = __shfl_sync(0xffffffffu, ti, 0);
+    if (whole_warp) v = make_int4(warp_uniform(v.x), warp_uniform(v.y), warp_uniform(v.z), warp_uniform(v.w));
     if (++rs == kTileRing) {
       rs = 0;
       rph ^= 1;
     }
-    return ti;
+    return Tile{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
   };
 
   if (warp == 0) {
@@ -350,7 +395,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
           }
           if (!ok) atomicOr(P.err, kErrBadTile);
         }
-        tile_ring[rs] = ok && ti < num_tiles ? ti : -1;
+        tile_ring[rs] = make_int4(ok && ti < num_tiles ? tile.pg : -1, tile.row0, tile.rows, tile.n0);
         mbar_arrive(&tile_full[rs]);
         if (++rs == kTileRing) {
           rs = 0;
@@ -405,9 +450,8 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
     uint32_t ph = 0, acc_ph = 0;
     bool any = false;
     while (true) {
-      const int ti = next_tile(true);
-      if (ti < 0) break;
-      const Tile& tile = P.tiles[ti];
+      const Tile tile = next_tile(true);
+      if (tile.pg < 0) break;
       const MxProblem& pr = P.prob[tile.pg >> 16];
       const int K = warp_uniform(pr.K);
       const bool two_b = warp_uniform(GATEUP || (tile.n0 + 128 < pr.N));
@@ -458,18 +502,16 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
   } else if (warp >= kMxProd1) {
     // --------------------------------------------------- copy threads 1, 2
     // B and its scale atoms: thread 1 the gate weights (down: all 256 rows, or
-    // the only 128), thread 2 the up weights (down: the atoms). Six copies a stage
-    // from one thread took 0.6 us. A copy may land before thread 0 announces the
-    // stage's bytes; the stage completes with both.
+    // the only 128), thread 2 the up weights (down: the atoms). A copy may land before
+    // thread 0 announces the stage's bytes; the stage completes with both.
     if (lane == 0) {
       const bool up = warp != kMxProd1;
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
       while (ok) {
-        const int ti = next_tile(false);
-        if (ti < 0) break;
-        const Tile tile = P.tiles[ti];
+        const Tile tile = next_tile(false);
+        if (tile.pg < 0) break;
         const int p = tile.pg >> 16, g = tile.pg & 0xFFFF;
         const MxProblem& pr = P.prob[p];
         const int kb = mx_kblocks(pr.K);
@@ -504,12 +546,10 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
     // 32-column chunks j = half * 32 + 64 c, which are whole MXFP8 groups
     const int quarter = warp & 3;
     const int half = (warp - 2) >> 2;
-    const int r = quarter * 32 + lane;
     uint32_t acc_ph = 0;
     while (true) {
-      const int ti = next_tile(true);
-      if (ti < 0) break;
-      const Tile tile = P.tiles[ti];
+      const Tile tile = next_tile(true);
+      if (tile.pg < 0) break;
       const MxProblem& pr = P.prob[tile.pg >> 16];
       const int wn = min(GATEUP ? 128 : 256, pr.N - tile.n0);
       int got = 1;
@@ -518,78 +558,17 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
       tc_fence_after_sync();
       acc_ph ^= 1;
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
-      uint32_t acc[2][32];
-      auto release_acc = [&]() {
-        tmem_ld_wait();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(acc_empty);
-      };
-      if (GATEUP) {
-        const bool valid = r < tile.rows;
-        const int grow = tile.row0 + r;
-        const int kbo = mx_kblocks(pr.N);
-        uint8_t* q = reinterpret_cast<uint8_t*>(pr.out) + static_cast<size_t>(grow) * pr.N + tile.n0;
+      // all of a thread's accumulator values first, so that the next tile's MMAs start before this one's arithmetic
+      uint32_t acc[4][32];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int j = half * 32 + 64 * c;
-          if (j < wn) {
-            tmem_ld_32x32b_x32(tbase + j, acc[0]);
-            tmem_ld_32x32b_x32(tbase + 128 + j, acc[1]);
-          }
-          if (c == 1) {
-            release_acc();
-          } else {
-            tmem_ld_wait();
-          }
-          if (j >= wn) continue;
-          float v[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            v[i] = gelu_tanh_exact(__uint_as_float(acc[0][i])) * __uint_as_float(acc[1][i]);
-          uint4 codes[2];
-          const uint32_t sc = mx_group(v, codes);
-          if (valid) {
-            reinterpret_cast<uint4*>(q + j)[0] = codes[0];
-            reinterpret_cast<uint4*>(q + j)[1] = codes[1];
-            pr.out_sf[mx_sf_offset(grow, (tile.n0 + j) / 32, kbo)] = static_cast<uint8_t>(sc);
-          }
-        }
-      } else {
-        // staged through the warp's buffer: whole-sector stores in row order
-        uint8_t* stg = sStg + (warp - 2) * kMxStgWarpBytes;
-        const int rows_valid = tile.rows - quarter * 32;
-        const size_t wrow = static_cast<size_t>(tile.row0 + quarter * 32);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int j = half * 32 + 64 * c;
-          if ((c & 1) == 0) {  // load chunks c, c + 1; after the second pair TMEM is no longer needed
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-              if (j + 64 * u < wn) tmem_ld_32x32b_x32(tbase + j + 64 * u, acc[u]);
-            if (c == 2) {
-              release_acc();
-            } else {
-              tmem_ld_wait();
-            }
-          }
-          if (j >= wn || rows_valid <= 0) continue;
-          uint32_t* a = acc[c & 1];
-          if (pr.out_f32) {
-            uint8_t* base = reinterpret_cast<uint8_t*>(reinterpret_cast<float*>(pr.out) + wrow * pr.ldo + tile.n0 + j);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) store_rows_32B(stg, a + 8 * q, lane, base + 32 * q, pr.ldo * 4, rows_valid);
-          } else {
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              pk[i] = pack_bf16x2(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
-            uint8_t* base =
-                reinterpret_cast<uint8_t*>(reinterpret_cast<__nv_bfloat16*>(pr.out) + wrow * pr.ldo + tile.n0 + j);
-            store_rows_bf16x32(stg, pk, lane, reinterpret_cast<__nv_bfloat16*>(base), pr.ldo, rows_valid);
-          }
-        }
-      }
+      for (int c = 0; c < 4; ++c)  // GATEUP: gate, up of columns half * 32 .., then of those 64 further
+        tmem_ld_32x32b_x32(tbase + half * 32 + (GATEUP ? 64 * (c >> 1) + 128 * (c & 1) : 64 * c), acc[c]);
+      tmem_ld_wait();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty);
+      mx_epilogue<GATEUP>(pr, acc, tile.rows - quarter * 32, tile.row0 + quarter * 32, tile.n0, wn, half, lane,
+                          sStg + (warp - 2) * kMxStgWarpBytes);
     }
   }
 
@@ -600,317 +579,6 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
     tc_fence_after_sync();
     tmem_dealloc(tmem_base, kTmemCols);
   }
-}
-
-// ------------------------------------------------- MXFP8 GEMM on SM pairs
-
-// The same GEMM for large batches on a cluster of two CTAs, as
-// grouped_gemm_pair_kernel: a pair tile is two 128-row blocks of one expert
-// (even CTA row0, odd CTA row1) and 256 accumulator columns; each CTA holds its
-// own A rows, half of B (GATEUP: the gate / the up columns; DOWN: 128 output
-// columns) and the scales of its rows and of all 256 columns in its TMEM. An SM
-// moves 32 KB per 128-K stage instead of 48 KB, which is what the single-SM kernel
-// waits for in large batches. All copies complete on the even CTA's stage barrier;
-// scale tiles are tensor copies too, as only those may complete on a peer's barrier.
-constexpr int kMxPStages = 6;
-constexpr int kMxPBBytes = 128 * kMxKStage;
-constexpr int kMxPStageBytes = kMxABytes + kMxPBBytes;
-constexpr int kMxPThreads = 32 * 11;  // copy, MMA, 8 epilogue, scale copy
-constexpr int kMxPSmemBytes = kMxPStages * (kMxPStageBytes + 3 * kMxSfBytes) + 8 * kMxStgWarpBytes + 1024 + 512;
-
-struct MxPairParams {
-  CUtensorMap tmA[2], tmAm[2], tmAs[2];  // as MxParams
-  CUtensorMap tmB0[2], tmB1[2];
-  CUtensorMap tmSa[2], tmSb0[2], tmSb1[2];  // scale tiles: rows of 128 words
-  MxProblem prob[2];
-  int nprob;
-  const Tile* tiles;
-  const int32_t* num_tiles;
-  uint32_t* err;
-};
-
-__device__ __forceinline__ void umma_mxf8_pair(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi,
-                                               uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "mov.b64 a, {%1, %2};\n\t"
-      "mov.b64 b, {%3, %4};\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.block32 [%0], a, b, %5, [%7], [%8], p;\n\t}" ::"r"(d),
-      "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
-      : "memory");
-}
-
-// tmem_cp_scales in both CTAs, each from its own shared memory
-__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint32_t saddr) {
-  asm volatile(
-      "{\n\t.reg .b64 a;\n\tmov.b64 a, {%1, %2};\n\ttcgen05.cp.cta_group::2.32x128b.warpx4 [%0], a;\n\t}" ::"r"(taddr),
-      "r"(saddr >> 4), "r"((128u >> 4) | (1u << 14))
-      : "memory");
-}
-__host__ __device__ constexpr uint32_t idesc_mxf8_m256(int n, int sf_id) {
-  return (static_cast<uint32_t>(sf_id) << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) |
-         (static_cast<uint32_t>(256 >> 4) << 24) | (static_cast<uint32_t>(sf_id) << 29);
-}
-
-template <bool GATEUP>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxPThreads, 1)
-    mx_gemm_pair_kernel(const __grid_constant__ MxPairParams P) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sA = smem;
-  uint8_t* sB = sA + kMxPStages * kMxABytes;
-  uint8_t* sSf = sB + kMxPStages * kMxPBBytes;  // per stage: A tile, B tiles 0 and 1
-  uint8_t* sStg = sSf + kMxPStages * 3 * kMxSfBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sStg + 8 * kMxStgWarpBytes);
-  uint64_t* empty = full + kMxPStages;
-  uint64_t* acc_full = empty + kMxPStages;
-  uint64_t* acc_empty = acc_full + 1;
-  uint64_t* drain = acc_empty + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-
-  const int warp = warp_uniform(threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
-  const bool leader = rank == 0;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kMxPStages; ++s) {
-      mbar_init(&full[s], 1);   // announced by the even CTA's copy thread; both CTAs' copies complete on it
-      mbar_init(&empty[s], 1);  // the MMA commit, in both CTAs
-    }
-    mbar_init(acc_full, 1);
-    mbar_init(acc_empty, 2 * 8);  // every epilogue warp of both CTAs
-    mbar_init(drain, 1);
-    *abort_flag = 0;
-    fence_mbar_init_cluster();
-  }
-  if (warp == 1) {
-    tmem_alloc_pair(tmem_slot, kTmemCols);
-    tmem_relinquish_pair();
-  }
-  tc_fence_before_sync();
-  cluster_sync();  // both CTAs' barriers initialised and TMEM allocated
-  tc_fence_after_sync();
-  const uint32_t tmem_base = *tmem_slot;
-  pdl_wait_then_release();
-  const int num_tiles = *P.num_tiles;
-  const uint32_t full_even = mapa_shared(&full[0], 0);
-  const uint32_t acc_empty_even = mapa_shared(acc_empty, 0);
-  // both CTAs walk the same tiles in the same order; a bad one ends the walk of every role in both
-  const int cid = static_cast<int>(cluster_id_x());
-  const int ncl = static_cast<int>(nclusters_x());
-  auto tile_ok = [&](const Tile& tile) -> bool {
-    const int p = tile.pg >> 16, g = tile.pg & 0xFFFF;
-    if (p >= P.nprob) return false;
-    const MxProblem& pr = P.prob[p];
-    return g < pr.groups && tile.row0 >= 0 && tile.row0 < pr.a_rows && !(tile.row0 & 127) && tile.n0 >= 0 &&
-           tile.n0 < pr.N && !(tile.n0 & 127) && tile.rows1 >= 0 &&
-           (tile.rows1 == 0 || (tile.row1 >= 0 && tile.row1 < pr.a_rows && !(tile.row1 & 127)));
-  };
-  auto a_box = [](int rows) -> int {  // rows of the A box that holds a block's rows
-    return rows <= 0 ? 0 : rows <= kMxASmallRows ? kMxASmallRows : rows <= kMxAMidRows ? kMxAMidRows : 128;
-  };
-
-  if (warp == 0 || warp == 10) {
-    // ------------------------------------------------- copies: 0 A and B, 10 scales
-    if (lane == 0) {
-      const bool scales = warp == 10;
-      int s = 0, issued = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      for (int ti = cid; ok && ti < num_tiles; ti += ncl) {
-        const Tile tile = P.tiles[ti];
-        if (!tile_ok(tile)) {
-          atomicOr(P.err, kErrBadTile);
-          break;
-        }
-        const int p = tile.pg >> 16, g = tile.pg & 0xFFFF;
-        const MxProblem& pr = P.prob[p];
-        const int kb = mx_kblocks(pr.K);
-        const bool two_b = GATEUP || (tile.n0 + 128 < pr.N);  // else the odd CTA's columns are all outside (and zero)
-        const int box0 = a_box(tile.rows), box1 = a_box(tile.rows1);
-        const int mine = leader ? box0 : box1, row = leader ? tile.row0 : tile.row1;
-        const uint32_t both = (box0 + box1) * kMxKStage + 2 * kMxPBBytes +
-                              kMxSfBytes * (1 + (box1 ? 1 : 0) + (two_b ? 4 : 2));
-        const CUtensorMap* ma = mine == kMxASmallRows ? &P.tmAs[p] : mine == kMxAMidRows ? &P.tmAm[p] : &P.tmA[p];
-        const CUtensorMap* mb = GATEUP && !leader ? &P.tmB1[p] : &P.tmB0[p];
-        const int col = tile.n0 + (GATEUP || leader ? 0 : 128);
-        const int sfa = (row >> 7) * kb;
-        const int sfb = (g * ((pr.N + 127) / 128) + (tile.n0 >> 7)) * kb;
-        for (int ks = 0; ks < kb; ++ks) {
-          if (!mbar_wait_cycles(&empty[s], ph ^ 1, abort_flag, P.err)) {
-            ok = false;
-            break;
-          }
-          const uint32_t bar = full_even + 8u * s;
-          if (!scales) {
-            if (leader) mbar_arrive_expect_tx(&full[s], both);
-            if (mine) tma_load_2d_pair(sA + s * kMxABytes, ma, bar, ks * kMxKStage, row);
-            tma_load_3d_pair(sB + s * kMxPBBytes, mb, bar, ks * kMxKStage, col, g);
-          } else {
-            uint8_t* sf = sSf + s * 3 * kMxSfBytes;
-            if (mine) tma_load_2d_pair(sf, &P.tmSa[p], bar, 0, sfa + ks);
-            tma_load_2d_pair(sf + kMxSfBytes, &P.tmSb0[p], bar, 0, sfb + ks);
-            if (two_b)
-              tma_load_2d_pair(sf + 2 * kMxSfBytes, GATEUP ? &P.tmSb1[p] : &P.tmSb0[p], bar, 0,
-                               sfb + (GATEUP ? 0 : kb) + ks);
-          }
-          ++issued;
-          if (++s == kMxPStages) {
-            s = 0;
-            ph ^= 1;
-          }
-        }
-      }
-      if (leader && !scales && *abort_flag) {  // copies of both CTAs still in flight complete on these barriers
-        const int pending = issued < kMxPStages ? issued : kMxPStages;
-        for (int i = 0; i < pending; ++i) {
-          if (--s < 0) {
-            s = kMxPStages - 1;
-            ph ^= 1;
-          }
-          uint32_t dummy = 0;
-          mbar_wait_cycles(&full[s], ph, reinterpret_cast<volatile int*>(&dummy), P.err, kWaitTimeoutCycles / 20);
-        }
-      }
-    }
-  } else if (warp == 1) {
-    if (leader) {
-      // -------------------------------------------------------- MMA issuer
-      int s = 0;
-      uint32_t ph = 0, acc_ph = 0;
-      for (int ti = cid; ti < num_tiles; ti += ncl) {
-        const Tile& tile = P.tiles[ti];
-        if (!warp_uniform(tile_ok(tile))) break;
-        const MxProblem& pr = P.prob[tile.pg >> 16];
-        const int K = warp_uniform(pr.K);
-        const bool two_b = warp_uniform(GATEUP || (tile.n0 + 128 < pr.N));
-        int free = 1;
-        if (lane == 0) free = mbar_wait_cluster(acc_empty, acc_ph ^ 1, abort_flag, P.err);
-        if (!warp_uniform(free)) break;
-        tc_fence_after_sync();
-        bool ok = true;
-        for (int k0 = 0; k0 < K; k0 += kMxKStage) {
-          if (!__all_sync(0xffffffffu, mbar_wait_cycles(&full[s], ph, abort_flag, P.err))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          const uint32_t al = desc_lo(smem_u32(sA + s * kMxABytes), 16), bl = desc_lo(smem_u32(sB + s * kMxPBBytes), 16);
-          const uint32_t slot = tmem_base + kAccCols + s * 16, sf = smem_u32(sSf + s * 3 * kMxSfBytes);
-          if (elect_one()) {
-            tmem_cp_scales_pair(slot, sf);
-            tmem_cp_scales_pair(slot + 4, sf + kMxSfBytes);
-            if (two_b) tmem_cp_scales_pair(slot + 8, sf + 2 * kMxSfBytes);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (j == 2 && K - k0 <= 64) break;
-              umma_mxf8_pair(tmem_base, al + j * 2, desc_hi(1024), bl + j * 2, desc_hi(1024), idesc_mxf8_m256(256, j),
-                             slot, slot + 4, j != 0 || k0 != 0);
-            }
-            umma_commit_pair(&empty[s], 0x3);  // frees the stage in both CTAs
-          }
-          __syncwarp();
-          if (++s == kMxPStages) {
-            s = 0;
-            ph ^= 1;
-          }
-        }
-        if (!ok) break;
-        if (elect_one()) umma_commit_pair(acc_full, 0x3);
-        acc_ph ^= 1;
-      }
-      if (elect_one()) umma_commit_pair(drain, 0x3);  // both CTAs learn when every MMA has completed
-      __syncwarp();
-    }
-  } else {
-    // ----------------------------------------------------------- epilogue, as mx_gemm_kernel; all 128 accumulator
-    // values of a thread are read first, so that the next tile's MMAs start before this one's arithmetic
-    const int quarter = warp & 3;
-    const int half = (warp - 2) >> 2;
-    uint8_t* stg = sStg + (warp - 2) * kMxStgWarpBytes;
-    uint32_t acc_ph = 0;
-    for (int ti = cid; ti < num_tiles; ti += ncl) {
-      const Tile tile = P.tiles[ti];
-      if (!tile_ok(tile)) break;
-      const MxProblem& pr = P.prob[tile.pg >> 16];
-      const int wn = min(GATEUP ? 128 : 256, pr.N - tile.n0);
-      int got = 1;
-      if (lane == 0) got = mbar_wait_cycles(acc_full, acc_ph, abort_flag, P.err);
-      if (!__shfl_sync(0xffffffffu, got, 0)) break;
-      tc_fence_after_sync();
-      acc_ph ^= 1;
-      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
-      const int t_rows = leader ? tile.rows : tile.rows1, t_row0 = leader ? tile.row0 : tile.row1;
-      const int rows_valid = t_rows - quarter * 32;  // of this warp's 32 rows
-      uint32_t acc[4][32];
-      if (rows_valid > 0) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)  // GATEUP: gate, up of columns half * 32 .., then of those 64 further
-          tmem_ld_32x32b_x32(tbase + half * 32 + (GATEUP ? 64 * (c >> 1) + 128 * (c & 1) : 64 * c), acc[c]);
-        tmem_ld_wait();
-      }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_even);
-      if (rows_valid <= 0) continue;
-      const size_t wrow = static_cast<size_t>(t_row0 + quarter * 32);
-      if (GATEUP) {
-        const int kbo = mx_kblocks(pr.N);
-        const int grow = t_row0 + quarter * 32 + lane;
-        uint8_t* q = reinterpret_cast<uint8_t*>(pr.out) + static_cast<size_t>(grow) * pr.N + tile.n0;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int j = half * 32 + 64 * c;
-          if (j >= wn) continue;
-          float v[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            v[i] = gelu_tanh_exact(__uint_as_float(acc[2 * c][i])) * __uint_as_float(acc[2 * c + 1][i]);
-          uint4 codes[2];
-          const uint32_t sc = mx_group(v, codes);
-          if (lane < rows_valid) {
-            reinterpret_cast<uint4*>(q + j)[0] = codes[0];
-            reinterpret_cast<uint4*>(q + j)[1] = codes[1];
-            pr.out_sf[mx_sf_offset(grow, (tile.n0 + j) / 32, kbo)] = static_cast<uint8_t>(sc);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int j = half * 32 + 64 * c;
-          if (j >= wn) continue;
-          uint32_t* a = acc[c];
-          if (pr.out_f32) {
-            uint8_t* base = reinterpret_cast<uint8_t*>(reinterpret_cast<float*>(pr.out) + wrow * pr.ldo + tile.n0 + j);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) store_rows_32B(stg, a + 8 * q, lane, base + 32 * q, pr.ldo * 4, rows_valid);
-          } else {
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              pk[i] = pack_bf16x2(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
-            store_rows_bf16x32(stg, pk, lane, reinterpret_cast<__nv_bfloat16*>(pr.out) + wrow * pr.ldo + tile.n0 + j,
-                               pr.ldo, rows_valid);
-          }
-        }
-      }
-    }
-  }
-
-  // ---------------------------------------------------------------- teardown
-  // No MMA may still write either CTA's TMEM, and no copy may still target
-  // either CTA's shared memory, when the pair deallocates and exits.
-  if (warp == 1 && lane == 0) {
-    uint32_t dummy = 0;
-    mbar_wait_cycles(drain, 0, reinterpret_cast<volatile int*>(&dummy), P.err);
-  }
-  __syncwarp();
-  tc_fence_before_sync();
-  cluster_sync();
-  tc_fence_after_sync();
-  if (warp == 1) tmem_dealloc_pair(tmem_base, kTmemCols);
 }
 
 }  // namespace moe

@@ -401,7 +401,7 @@ def test_more_choices_than_the_few_token_form_holds():
 @pytest.mark.parametrize("T,k", [(160, 8), (257, 8), (700, 3)])
 @pytest.mark.parametrize("fed", [False, True])
 def test_block_of_many_rows_per_expert(D, F, S, T, k, fed):
-    """Experts with 160 routed rows and more on average, some with few or none (SM pairs)."""
+    """Experts with 160 routed rows and more on average, some with few or none."""
     dims = inputs.Dims(D, 8, F, S)
     w, dw = weights(dims), device_weights(dims)
     mw = block.quantize_mxfp8(dw)
