@@ -353,8 +353,10 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
-  pdl_wait_then_release();
-  const int num_tiles = *P.num_tiles;
+  // The kernel may start while the one that makes A runs (the scatter; for down the gate|up GEMM): that one has passed
+  // its own wait, so the tile list of the scan before it is there. Weights and tiles are read ahead, only thread 0, which
+  // copies A, waits; nothing is computed or written without A. (4 us of 162 at T = 64. The list is read past L1, which may
+  // hold an earlier call's.)
   // Tiles: the producer takes their indices from the work counter and publishes the tiles in the ring (pg, row0, rows,
   // n0; pg -1 ends the work), the other roles read them in order.
   int rs = 0;
@@ -380,14 +382,17 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
       // ------------------------------------------------------ TMA producer
       int s = 0, issued = 0;
       uint32_t ph = 0;
+      bool waited = false;
+      const int num_tiles = __ldcg(P.num_tiles);
       int ti = atomicAdd(P.next_tile, 1);
       while (true) {
         if (!mbar_wait_cycles(&tile_empty[rs], rph ^ 1, abort_flag, P.err)) break;
-        const Tile tile = ti < num_tiles ? P.tiles[ti] : Tile{};
+        const int4 tv = ti < num_tiles ? __ldcg(reinterpret_cast<const int4*>(P.tiles + ti)) : make_int4(-1, 0, 0, 0);
+        const Tile tile{tv.x, tv.y, tv.z, tv.w, 0, 0, 0, 0};
         const int p = tile.pg >> 16, g = tile.pg & 0xFFFF;
         bool ok = true;
         if (ti < num_tiles) {  // checked before the other roles see the tile
-          ok = p < P.nprob;
+          ok = tile.pg >= 0 && p < P.nprob;
           if (ok) {
             const MxProblem& pr = P.prob[p];
             ok = g < pr.groups && tile.row0 >= 0 && tile.row0 < pr.a_rows && !(tile.row0 & 127) && tile.n0 >= 0 &&
@@ -395,13 +400,15 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
           }
           if (!ok) atomicOr(P.err, kErrBadTile);
         }
-        tile_ring[rs] = make_int4(ok && ti < num_tiles ? tile.pg : -1, tile.row0, tile.rows, tile.n0);
+        tile_ring[rs] = ok ? tv : make_int4(-1, 0, 0, 0);
         mbar_arrive(&tile_full[rs]);
         if (++rs == kTileRing) {
           rs = 0;
           rph ^= 1;
         }
         if (!ok || ti >= num_tiles) break;
+        if (!waited) pdl_wait_then_release();
+        waited = true;
         const int next = atomicAdd(P.next_tile, 1);  // its latency hides behind this tile's loads
         const MxProblem& pr = P.prob[p];
         const int kb = mx_kblocks(pr.K);
