@@ -27,13 +27,17 @@
 // after the start at T = 1).
 //
 // Products: tcgen05.mma with the weight columns as M = 128 and the tokens as
-// N = 16, one thread issuing 8 or 16 MMAs per chunk, so the SM's issue slots play no
+// N = 16, one lane issuing 8 MMAs per chunk, so the SM's issue slots play no
 // part. (With mma.sync on eight warps - M = 16 tiles of columns, N = 8 or 16 -
 // the MXFP8 form executed 136 instructions per 32 K of a warp's tile and took
 // 155 us at T = 8; its chunks cost 1.9 us each against 0.75 us of HBM time.)
 // Every token's column is computed for every touched expert; a token takes an
 // expert's result only if it is routed there (a select, so that nothing of an
 // expert reaches other tokens).
+//
+// Measured (embed 2816, 128 experts of 704, top-8, shared 2112; of the measured copy rate): bf16 T = 1 43 us (46%),
+// 5 with norms 104 us (67%), 16 173 us (90%: 972 MB from HBM); MXFP8 T = 1 37 us, 8 72 us (72%). What does not
+// stream is fixed: the small kernel and the gap to this one 6 us, the hand-over to D 7 us, the output 4 us.
 //
 // Numerics: fp32 accumulation. bf16 form: the GeGLU rows enter the down product as
 // the sum of two bf16 values (hi + lo, 16 bits of mantissa), the routed sums are
@@ -447,7 +451,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   tc_fence_after_sync();
   // The next kernel may be set up from now on (the library's wait for this one's end before they touch memory).
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
 
   if (warp < kFewProdWarps || warp == kFewProdWarp4) {
     const int role = warp == kFewProdWarp4 ? 4 : warp;

@@ -16,6 +16,12 @@
 // 200 -> 193 us without). The four 32-K MMAs of the stage pick their byte of the
 // slot's words by the scale id of the instruction descriptor. A reduction that ends inside a stage (K a multiple
 // of 64) issues only the MMAs it has.
+//
+// The MMA thread's own instructions set the pace where HBM does not: with descriptors built per MMA and one lane in the
+// loops a stage took 770 cycles to issue (its MMAs run 512); a uniform warp with one elected lane takes 310 (T = 4096
+// gate|up 256 -> 188 us, down 157 -> 132 us). At T = 4096 gate|up keeps the tensor pipe 66% busy; down, with 6 stages a
+// tile and TMEM for one 256-column accumulator beside the scales, 40%. At T = 64 the two stream the weights at 80% of
+// the measured copy rate.
 #pragma once
 
 #include "grouped_gemm.cuh"
@@ -85,8 +91,8 @@ __global__ void mx_act_quant_kernel(const __nv_bfloat16* __restrict__ x, size_t 
 // groups. Written: the codes and scale atoms of the token's k routed rows, the
 // token-order scale atoms (the shared MLP's), and - without xq, which the shared
 // MLP reads in place - the token-order codes. The blocks of a grid column (y) take
-// every gridDim.y-th 32 groups: large batches have three, as one warp per token left
-// too few loads in flight (T = 4096 38 us).
+// every gridDim.y-th 32 groups: with one warp for a whole row too few loads were in
+// flight (T = 4096 38 us; now 35 us for 115 MB, written as 16-byte pieces of scattered rows).
 __global__ void __launch_bounds__(256) route_scatter_mx_kernel(
     const int32_t* __restrict__ idx, const uint32_t* __restrict__ masks, const int32_t* __restrict__ base, int T,
     int k, int E, int D, const __nv_bfloat16* __restrict__ x, const uint8_t* __restrict__ xq,

@@ -14,6 +14,8 @@ to be read against the pages:
 * ``nvfp4``     - e2m1 / e4m3 codecs and the group-16 NVFP4 quantiser;
 * ``wformats``  - the weight-only formats SFP8 and Q4_0 (readings stated in
   the module) and the block on weights in those formats;
+* ``mxfp8``     - e4m3 / e8m0 codecs, the group-of-32 MXFP8 quantiser, its scale
+  tiles and the block on MXFP8 weights and activations;
 * ``sandwich``  - the pre/post-FFN RMSNorm sandwich and residual;
 * ``counts``    - parameter counts implied by the layer shapes.
 
