@@ -19,9 +19,10 @@
 //
 // The MMA thread's own instructions set the pace where HBM does not: with descriptors built per MMA and one lane in the
 // loops a stage took 770 cycles to issue (its MMAs run 512); a uniform warp with one elected lane takes 310 (T = 4096
-// gate|up 256 -> 188 us, down 157 -> 132 us). At T = 4096 gate|up keeps the tensor pipe 66% busy; down, with 6 stages a
-// tile and TMEM for one 256-column accumulator beside the scales, 40%. At T = 64 the two stream the weights at 80% of
-// the measured copy rate.
+// gate|up 256 -> 188 us, down 157 -> 132 us). What is left at T = 4096 is shared memory: a stage writes 48 KB and its
+// MMAs read 48 KB, 768 cycles at 128 bytes a cycle against 512 of MMA, and gate|up takes 812 a stage (tensor pipe 66%
+// busy); down adds the epilogue's staging and, with 6 stages a tile and TMEM for one 256-column accumulator beside the
+// scales, waits for its epilogue (40%). At T = 64 the two stream the weights at 80% of the measured copy rate.
 #pragma once
 
 #include "grouped_gemm.cuh"
@@ -92,7 +93,8 @@ __global__ void mx_act_quant_kernel(const __nv_bfloat16* __restrict__ x, size_t 
 // token-order scale atoms (the shared MLP's), and - without xq, which the shared
 // MLP reads in place - the token-order codes. The blocks of a grid column (y) take
 // every gridDim.y-th 32 groups: with one warp for a whole row too few loads were in
-// flight (T = 4096 38 us; now 35 us for 115 MB, written as 16-byte pieces of scattered rows).
+// flight. A store instruction of the warp covers 512 contiguous bytes of a row (each lane storing its own two pieces
+// left half of every sector to the next instruction: T = 4096 35 us; now 26 us for 115 MB, 68% of the copy rate).
 __global__ void __launch_bounds__(256) route_scatter_mx_kernel(
     const int32_t* __restrict__ idx, const uint32_t* __restrict__ masks, const int32_t* __restrict__ base, int T,
     int k, int E, int D, const __nv_bfloat16* __restrict__ x, const uint8_t* __restrict__ xq,
@@ -125,38 +127,52 @@ __global__ void __launch_bounds__(256) route_scatter_mx_kernel(
     for (int g0 = blockIdx.y * 32; g0 < ng; g0 += 32 * gridDim.y) {
       const int g = g0 + lane;
       const bool in = g < ng;
-      uint4 codes[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+      // the 32 groups as 64 pieces of 16 bytes: pieces `lane` and 32 + lane are this lane's to store
+      const int p0 = 2 * g0 + lane, p1 = p0 + 32;
+      const bool in0 = p0 < 2 * ng, in1 = p1 < 2 * ng;
+      uint4 c0 = make_uint4(0, 0, 0, 0), c1 = c0;
       uint32_t sc = 0;
-      if (in) {
-        if (xq) {
-          const uint4* src = reinterpret_cast<const uint4*>(xq + static_cast<size_t>(t) * D) + 2 * g;
-          codes[0] = __ldg(src);
-          codes[1] = __ldg(src + 1);
-          sc = __ldg(xs + static_cast<size_t>(t) * ng + g);
-        } else {
+      if (xq) {
+        const uint4* src = reinterpret_cast<const uint4*>(xq + static_cast<size_t>(t) * D);
+        if (in0) c0 = __ldg(src + p0);
+        if (in1) c1 = __ldg(src + p1);
+        if (in) sc = __ldg(xs + static_cast<size_t>(t) * ng + g);
+      } else {
+        uint4 codes[2] = {c0, c0};
+        if (in) {
           float v[32];
           load32_bf16(x + static_cast<size_t>(t) * D + g * kMxGroup, v);
           sc = mx_group(v, codes);
         }
+        // lane l has pieces 2 l and 2 l + 1
+        const int from = lane >> 1;
+        auto piece = [&](int lane_of) -> uint4 {
+          const uint4 a = codes[0], b = codes[1];
+          uint4 lo, hi;
+          lo.x = __shfl_sync(0xffffffffu, a.x, lane_of), hi.x = __shfl_sync(0xffffffffu, b.x, lane_of);
+          lo.y = __shfl_sync(0xffffffffu, a.y, lane_of), hi.y = __shfl_sync(0xffffffffu, b.y, lane_of);
+          lo.z = __shfl_sync(0xffffffffu, a.z, lane_of), hi.z = __shfl_sync(0xffffffffu, b.z, lane_of);
+          lo.w = __shfl_sync(0xffffffffu, a.w, lane_of), hi.w = __shfl_sync(0xffffffffu, b.w, lane_of);
+          return lane & 1 ? hi : lo;
+        };
+        c0 = piece(from);
+        c1 = piece(16 + from);
+        uint4* qt = reinterpret_cast<uint4*>(xq_tok + static_cast<size_t>(t) * D);
+        if (in0) qt[p0] = c0;
+        if (in1) qt[p1] = c1;
       }
       // the four scales of a 128-K block are one aligned word of the atom
       uint32_t scw = sc << (8 * (lane & 3));
       scw |= __shfl_xor_sync(0xffffffffu, scw, 1);
       scw |= __shfl_xor_sync(0xffffffffu, scw, 2);
-      if (!in) continue;
-      const bool word = (lane & 3) == 0;
-      if (!xq) {
-        uint4* qt = reinterpret_cast<uint4*>(xq_tok + static_cast<size_t>(t) * D) + 2 * g;
-        qt[0] = codes[0];
-        qt[1] = codes[1];
-      }
+      const bool word = in && (lane & 3) == 0;
       if (word) *reinterpret_cast<uint32_t*>(xsf_tok + mx_sf_offset(t, g, kb)) = scw;
       for (int j = 0; j < k; ++j) {
         const int row = s_rows[wid][j];
         if (row < 0) continue;
-        uint4* qp = reinterpret_cast<uint4*>(xq_perm + static_cast<size_t>(row) * D) + 2 * g;
-        qp[0] = codes[0];
-        qp[1] = codes[1];
+        uint4* qp = reinterpret_cast<uint4*>(xq_perm + static_cast<size_t>(row) * D);
+        if (in0) qp[p0] = c0;
+        if (in1) qp[p1] = c1;
         if (word) *reinterpret_cast<uint32_t*>(xsf_perm + mx_sf_offset(row, g, kb)) = scw;
       }
     }
