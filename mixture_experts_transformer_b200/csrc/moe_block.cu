@@ -2139,6 +2139,7 @@ moe_status moe_add_rms_norm(const moe_norm_params* p, void* stream) {
   const AddNormParams P{p->T,
                         D,
                         eps,
+                        1.0 / D,
                         static_cast<const __nv_bfloat16*>(p->x),
                         static_cast<const __nv_bfloat16*>(p->residual),
                         static_cast<const __nv_bfloat16*>(p->gamma_post),

@@ -72,7 +72,8 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_rows_kernel(const __nv_
 //   y[t] = gamma s[t] / rms(s[t]),   rms(v) = sqrt(mean(v^2) + eps)
 //
 // in fp32; sum = RNE_bf16(s), y = RNE_bf16(y), q / scale = MXFP8(y) from the
-// fp32 y (one rounding each). Memory bound: 4 bytes in and up to 5 + 1/32 out
+// fp32 y (one rounding each), and where fp32 leaves a code open from y in 64
+// bits (exact_codes). Memory bound: 4 bytes in and up to 5 + 1/32 out
 // per element, the row held in registers between the passes. A row belongs to
 // TPR threads, each with NV 8-column vectors: a warp per row up to 1024
 // columns (no block barrier, and small rows fill the warp), 128 threads up to
@@ -80,14 +81,16 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_rows_kernel(const __nv_
 // maximum takes two shuffles. Sums: a thread's squares in order, a fixed
 // xor tree, the warps in order - the same bits on every run.
 // The loads are plain (not the read-only path): sum may overwrite residual or x in place.
+// (The sum over a thread's columns is fp32, everything after it 64 bits.)
 template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float* s_red) {
+__device__ __forceinline__ double row_sum(float part, double* s_red) {
+  double v = part;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if constexpr (TPR > 32) {
     if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = 0.f;
+    v = 0.0;
 #pragma unroll
     for (int i = 0; i < TPR / 32; ++i) v += s_red[i];
   }
@@ -97,6 +100,7 @@ __device__ __forceinline__ float row_sum(float v, float* s_red) {
 struct AddNormParams {
   int T, D;
   float eps;
+  double inv_d;  // 1 / D
   const __nv_bfloat16* x;
   const __nv_bfloat16* residual;
   const __nv_bfloat16* gamma_post;
@@ -110,8 +114,8 @@ struct AddNormParams {
 // Two fp32 values in a 64-bit register pair, handled by the packed fp32
 // instructions: with one instruction per value the kernel spent 62% of its
 // issue slots and 78 us on 16384 rows of 2816 (every output), at 4.7 TB/s; it
-// now takes 70 us there (5.9 TB/s, 90% of the measured copy rate) and 20 us on
-// 4096 rows.
+// now takes 73 us there (5.7 TB/s, 87% of the measured copy rate; 70 us
+// without exact_codes, whose few warps end last) and 21 us on 4096 rows.
 using f32x2 = unsigned long long;
 __device__ __forceinline__ f32x2 pack2(float lo, float hi) {
   f32x2 r;
@@ -151,17 +155,55 @@ __device__ __forceinline__ float max_abs(float m, float v) {
   return r;
 }
 
+// The codes of a lane's eight values (s of 8-column vector v) and its group's scale code, decided in 64 bits. All lanes of
+// a warp together. e4m3 has 3 mantissa bits, so an fp32 value a few units from the middle of two codes can land on the
+// wrong side of it, which is a whole code step; the kernel comes here for the warps that hold such a value (0.2% of
+// them), or a group maximum as near to 1.75 2^e. (Only rows of finite values and sums get here.)
+__device__ __noinline__ void exact_codes(const AddNormParams& P, size_t row, int v, bool in, double ss, f32x2 s0,
+                                         f32x2 s1, f32x2 s2, f32x2 s3) {
+  const double a = ss * P.inv_d + static_cast<double>(P.eps), r0 = 1.0f / sqrtf(static_cast<float>(a));
+  const double r = r0 * (1.5 - 0.5 * a * r0 * r0);  // a Newton step on fp32's: good to 2^-44
+  uint4 gv = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+  if (P.gamma && in) gv = __ldg(reinterpret_cast<const uint4*>(P.gamma) + v);
+  const __nv_bfloat16* g = reinterpret_cast<const __nv_bfloat16*>(&gv);
+  float f[8];
+  unpack2(s0, f[0], f[1]);
+  unpack2(s1, f[2], f[3]);
+  unpack2(s2, f[4], f[5]);
+  unpack2(s3, f[6], f[7]);
+  double y[8], top = 0.0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    y[i] = f[i] * (r * __bfloat162float(g[i]));
+    top = fmax(top, fabs(y[i]));
+  }
+  top = fmax(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = fmax(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const long long b = __double_as_longlong(top);
+  const int c = static_cast<int>(b >> 52) - 1023 + 127 - 8 + ((b & 0xFFFFFFFFFFFFFll) > 0xC000000000000ll ? 1 : 0);
+  const uint32_t sc = c < 0 ? 0u : static_cast<uint32_t>(c);
+  const double inv = mx_inv_scale(sc);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {  // to fp32 rounded to odd, so that the rounding to e4m3 is the only one
+    const double w = y[i] * inv;
+    const float z = __double2float_rz(w);
+    f[i] = static_cast<double>(z) == w ? z : __uint_as_float(__float_as_uint(z) | 1u);
+  }
+  if (!in) return;
+  reinterpret_cast<uint2*>(P.q + row)[v] = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+  if ((v & 3) == 0) P.scale[(row >> 5) + (v >> 2)] = static_cast<uint8_t>(sc);
+}
+
 template <int TPR, int NV>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rms_norm_kernel(const AddNormParams P) {
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rms_norm_kernel(const __grid_constant__ AddNormParams P) {
   constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
-  __shared__ float s_red[2][TPR / 32];
+  __shared__ double s_red[2][TPR / 32];
   pdl_wait_then_release();
   const int lane = threadIdx.x % TPR;
   const int t = blockIdx.x * kRows + threadIdx.x / TPR;
   if (t >= P.T) return;  // TPR < 128 only: whole warps, no block barrier follows
   const int nvec = P.D >> 3;
   const size_t row = static_cast<size_t>(t) * P.D;
-  const float inv_d = 1.0f / static_cast<float>(P.D);
   uint4 xv[NV], rv[NV];
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
@@ -183,8 +225,8 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rms_norm_kernel(con
 #pragma unroll
     for (int i = 0; i < 4; ++i) s[u][i] = bf16x2_to_f32x2(w[i]);
   }
-  // 1 / rms of the row in s (elements past D are zero)
-  auto inv_rms = [&](float* red) -> float {
+  // the sum of squares of the row in s (elements past D are zero), and 1 / rms
+  auto sum_squares = [&](double* red) -> double {
     f32x2 ss = pack2(0.f, 0.f);
 #pragma unroll
     for (int u = 0; u < NV; ++u)
@@ -192,10 +234,11 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rms_norm_kernel(con
       for (int i = 0; i < 4; ++i) ss = fma2(s[u][i], s[u][i], ss);
     float lo, hi;
     unpack2(ss, lo, hi);
-    return 1.0f / sqrtf(row_sum<TPR>(lo + hi, red) * inv_d + P.eps);
+    return row_sum<TPR>(lo + hi, red);
   };
+  auto inv_rms = [&](double ss) -> float { return 1.0f / sqrtf(static_cast<float>(ss * P.inv_d) + P.eps); };
   if (P.gamma_post) {
-    const float r1 = inv_rms(s_red[0]);
+    const float r1 = inv_rms(sum_squares(s_red[0]));
     const f32x2 r = pack2(r1, r1);
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
@@ -203,11 +246,12 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rms_norm_kernel(con
       if (v >= nvec) continue;  // (stays zero)
       const uint4 gv = __ldg(reinterpret_cast<const uint4*>(P.gamma_post) + v);
       const uint32_t* g = reinterpret_cast<const uint32_t*>(&gv);
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&rv[u]);  // (zero without a residual)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[u][i] = mul2(mul2(s[u][i], r), bf16x2_to_f32x2(g[i]));
+      for (int i = 0; i < 4; ++i)  // the product of two bf16 is exact in fp32: one rounding
+        s[u][i] = fma2(mul2(s[u][i], bf16x2_to_f32x2(g[i])), r, bf16x2_to_f32x2(w[i]));
     }
-  }
-  if (P.residual) {
+  } else if (P.residual) {
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       const uint32_t* w = reinterpret_cast<const uint32_t*>(&rv[u]);
@@ -225,8 +269,10 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rms_norm_kernel(con
     }
   }
   if (!P.y && !P.q) return;
-  const float r1 = inv_rms(s_red[1]);
+  const double ss = sum_squares(s_red[1]);
+  const float r1 = inv_rms(ss);
   const f32x2 r = pack2(r1, r1);
+  uint32_t near = 0;  // bit u: vector u holds a value that fp32 leaves open
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
     const int v = lane + u * TPR;
@@ -259,12 +305,24 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rms_norm_kernel(con
       const f32x2 inv = pack2(i1, i1);
 #pragma unroll
       for (int i = 0; i < 4; ++i) unpack2(mul2(o[i], inv), f[2 * i], f[2 * i + 1]);
+      // a value within 4 units of the middle of two codes (r, s r and the product with gamma err by less), or a maximum
+      // as near to where the scale changes
+      constexpr uint32_t kNear = 4;
+      uint32_t off = ((m & 0x7FFFFFu) - 0x600000u + kNear) & 0x7FFFFFu;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) off = min(off, (__float_as_uint(f[i]) - 0x80000u + kNear) & 0xFFFFFu);
+      if (off <= 2 * kNear) near |= 1u << u;
       if (in) {
         reinterpret_cast<uint2*>(P.q + row)[v] = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
         if ((v & 3) == 0) P.scale[static_cast<size_t>(t) * (P.D >> 5) + (v >> 2)] = static_cast<uint8_t>(sc);
       }
     }
   }
+  if (!P.q) return;
+#pragma unroll
+  for (int u = 0; u < NV; ++u)
+    if (__any_sync(0xffffffffu, (near >> u) & 1u))
+      exact_codes(P, row, lane + u * TPR, lane + u * TPR < nvec, ss, s[u][0], s[u][1], s[u][2], s[u][3]);
 }
 
 }  // namespace moe

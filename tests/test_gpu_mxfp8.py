@@ -416,3 +416,40 @@ def test_block_of_many_rows_per_expert(D, F, S, T, k, fed):
                               router_bias=None if bias is None else torch.from_numpy(bias).cuda())
     ok()
     check_block(w, xb, res, k, bias, xv)
+
+
+@pytest.mark.parametrize("T,D", [(700, 2816), (3000, 256), (300, 4096), (64, 16384)])
+def test_add_norm_codes_are_those_of_64_bits(T, D):
+    """Codes and scales of y are the float64 oracle's: where an fp32 y lies within a few units of the middle of two codes
+    the kernel decides in 64 bits. What is left is the row's sum of squares: fp32 chains of at most 16 fused additions and
+    one more, then 64 bits, so at most 17 2^-24 of it and half of that in y. s = residual + x is exact in fp32 here, or
+    too small to move a code. (The first run: 2 codes of a million differ, 5e-9 from the middle.)"""
+    rng = np.random.default_rng(T)
+    xb, rb = inputs.make_x(T, D, seed=T), inputs.make_x(T, D, seed=T + 1)
+    gb = inputs.f32_to_bf16_bits((1 + 0.1 * rng.standard_normal(D)).astype(np.float32))
+    codes, q, j, scale, y = _codes(xb, rb, gb)
+    np.testing.assert_array_equal(scale, j)
+    other = codes != q
+    w = np.abs(y / np.exp2(np.repeat(j, 32, -1).astype(np.float64)))[other]
+    assert np.all(np.abs(w - (np.abs(codes) + np.abs(q))[other] / 2) <= 9 * 2.0**-24 * w)
+
+
+def _codes(xb, rb, gb):
+    res = block.add_rms_norm(block.bf16_tensor(xb), block.bf16_tensor(gb), residual=block.bf16_tensor(rb), quantize=True)
+    ok()
+    s = mo.f64(xb) + mo.f64(rb)
+    y = mo.f64(gb) * s / np.sqrt((s * s).mean(-1, keepdims=True) + 1e-6)
+    q, j = mx.quantize(y)
+    return to_np(res.q.float()).astype(np.float64), q, j, to_np(res.scale.view(torch.uint8)).astype(int) - 127, y
+
+
+@pytest.mark.parametrize("T,D", [(700, 2816), (3000, 256), (300, 4096), (64, 16384)])
+def test_add_norm_codes_of_whole_numbers(T, D):
+    """Whole numbers up to 16: their sums of squares are exact in fp32 (at most 2^8 each, 2^14 of them), so every code
+    and scale is the oracle's."""
+    rng = np.random.default_rng(D)
+    xb, rb = (inputs.f32_to_bf16_bits(rng.integers(-8, 9, (T, D)).astype(np.float32)) for _ in range(2))
+    gb = inputs.f32_to_bf16_bits((1 + 0.1 * rng.standard_normal(D)).astype(np.float32))
+    codes, q, j, scale, _ = _codes(xb, rb, gb)
+    np.testing.assert_array_equal(scale, j)
+    assert np.count_nonzero(codes != q) == 0
