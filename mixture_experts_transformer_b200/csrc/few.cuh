@@ -35,8 +35,8 @@
 // expert's result only if it is routed there (a select, so that nothing of an
 // expert reaches other tokens).
 //
-// Measured (embed 2816, 128 experts of 704, top-8, shared 2112; of the measured copy rate): bf16 T = 1 43 us (46%),
-// 5 with norms 104 us (67%), 16 173 us (90%: 972 MB from HBM); MXFP8 T = 1 37 us, 8 72 us (72%). What does not
+// Measured (embed 2816, 128 experts of 704, top-8, shared 2112; of the measured copy rate): bf16 T = 1 45 us (45%),
+// 5 with norms 106 us (66%), 16 173-187 us (83-90%: 972 MB from HBM); MXFP8 T = 1 37 us, 8 70 us (73%). What does not
 // stream is fixed: the small kernel and the gap to this one 6 us, the hand-over to D 7 us, the output 4 us.
 //
 // Numerics: fp32 accumulation. bf16 form: the GeGLU rows enter the down product as
