@@ -218,9 +218,9 @@ __device__ __forceinline__ void few_umma_bf16(uint32_t d, uint32_t alo, uint32_t
       "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// fp32 as an unsigned integer of the same order (a positive NaN above infinity)
+// fp32 (no NaN) as an unsigned integer of the same order; zeros of either sign are equal, -infinity is above 0
 __device__ __forceinline__ uint32_t order_key(float v) {
-  const uint32_t b = __float_as_uint(v);
+  const uint32_t b = v == 0.f ? 0u : __float_as_uint(v);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
@@ -750,7 +750,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (in && P.bias) l[h][i] += __ldg(P.bias + e4 + i);
-          key[h][i] = in ? max(order_key(l[h][i] + 0.f), 1u) : 0u;  // (-0 + 0 = +0); key 0: not to be taken
+          // a NaN counts as -infinity, as in the block's own routing; key 0: not to be taken
+          key[h][i] = in ? order_key(isnan(l[h][i]) ? -INFINITY : l[h][i]) : 0u;
           if (in && h < ntok && cta == 0 && P.logits_out)
             P.logits_out[static_cast<size_t>(wr + 8 * h) * P.E + e4 + i] = l[h][i];
         }

@@ -1,0 +1,79 @@
+"""Edges of the few-token layer and the MXFP8 block on a B200: selection, alignment, streams, limits."""
+
+import dataclasses
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_common import SMALL, device_weights, require_gpu, to_np, weights
+from mixture_experts_transformer_b200 import binding as B
+from mixture_experts_transformer_b200 import block, inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def ok():
+    st = B.moe_get_device_status()
+    assert st == B.MOE_OK, B.moe_status_string(st)
+
+
+# ------------------------------------------------------------- selection
+
+
+@pytest.mark.parametrize("T", [1, 8, 16])
+@pytest.mark.parametrize("k", [1, 4, 15, 16])
+@pytest.mark.parametrize("where", ["router", "bias", "-bias"])
+def test_a_nan_logit_never_wins(T, k, where):
+    """Logits that are NaN: every entry counts them as minus infinity, as the whole block does (experts 3 and 11 are
+    chosen only when all 16 are, last and in order)."""
+    w, dw = weights(SMALL), device_weights(SMALL)
+    x = block.bf16_tensor(inputs.make_x(T, SMALL.embed_dim, seed=T))
+    bias = None
+    if where == "router":
+        router = w.w_router.copy()
+        router[5, 3], router[200, 11] = 0x7FC0, 0xFFC0
+        dw = dataclasses.replace(dw, w_router=block.bf16_tensor(router))
+    else:
+        bias = torch.zeros(SMALL.num_experts, device="cuda")
+        bias[[3, 11]] = float("nan")
+        if where == "-bias":
+            bias.view(torch.int32)[[3, 11]] = -4194304  # 0xFFC00000
+    ref = block.forward(dw, x, top_k=k, router_bias=bias, debug=True)
+    got = block.forward_few(dw, x, top_k=k, router_bias=bias, debug=True)
+    mx = block.forward_mxfp8(block.quantize_mxfp8(dw), x, top_k=k, router_bias=bias, debug=True)
+    ok()
+    for res in (got, mx):
+        assert torch.equal(res.idx, ref.idx)
+        np.testing.assert_allclose(to_np(res.w), to_np(ref.w), rtol=2e-5, atol=1e-9)
+        assert torch.isfinite(res.out_f32).all()
+        assert torch.equal(res.cnt, ref.cnt)
+    assert torch.equal(torch.isnan(got.logits), torch.isnan(ref.logits))
+    hit = torch.isin(ref.idx, torch.tensor([3, 11], device="cuda"))
+    assert bool(hit.any()) == (k > 14) and torch.all(ref.w[hit] == 0)
+
+
+@pytest.mark.parametrize("T", [1, 16])
+def test_infinite_logits_choose_as_the_whole_block(T):
+    """+infinity first, -infinity and NaN last and in order; only NaN logits: the first k experts, weights NaN."""
+    dw = device_weights(SMALL)
+    x = block.bf16_tensor(inputs.make_x(T, SMALL.embed_dim, seed=T))
+    mw = block.quantize_mxfp8(dw)
+    inf, nan = float("inf"), float("nan")
+    for values in ({2: -inf, 5: nan, 9: -inf}, {7: inf}, {4: inf, 9: inf, 1: nan}, {e: nan for e in range(16)}):
+        bias = torch.zeros(SMALL.num_experts, device="cuda")
+        for e, v in values.items():
+            bias[e] = v
+        for k in (2, 16):
+            ref = block.forward(dw, x, top_k=k, router_bias=bias, debug=True)
+            got = block.forward_few(dw, x, top_k=k, router_bias=bias, debug=True)
+            mx = block.forward_mxfp8(mw, x, top_k=k, router_bias=bias, debug=True)
+            ok()
+            for res in (got, mx):
+                assert torch.equal(res.idx, ref.idx)
+                np.testing.assert_allclose(to_np(res.w), to_np(ref.w), rtol=2e-5, atol=1e-9)
