@@ -158,7 +158,8 @@ __device__ __forceinline__ float max_abs(float m, float v) {
 // The codes of a lane's eight values (s of 8-column vector v) and its group's scale code, decided in 64 bits. All lanes of
 // a warp together. e4m3 has 3 mantissa bits, so an fp32 value a few units from the middle of two codes can land on the
 // wrong side of it, which is a whole code step; the kernel comes here for the warps that hold such a value (0.2% of
-// them), or a group maximum as near to 1.75 2^e. (Only rows of finite values and sums get here.)
+// them), or a group maximum as near to 1.75 2^e. (Only rows of finite s and sums get here; a group of the warp may be NaN through
+// gamma.)
 __device__ __noinline__ void exact_codes(const AddNormParams& P, size_t row, int v, bool in, double ss, f32x2 s0,
                                          f32x2 s1, f32x2 s2, f32x2 s3) {
   const double a = ss * P.inv_d + static_cast<double>(P.eps), r0 = 1.0f / sqrtf(static_cast<float>(a));
@@ -175,13 +176,14 @@ __device__ __noinline__ void exact_codes(const AddNormParams& P, size_t row, int
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     y[i] = f[i] * (r * __bfloat162float(g[i]));
-    top = fmax(top, fabs(y[i]));
+    // past fp32's largest value, or NaN (a gamma that is not finite): the group is NaN, as in fp32
+    top = fabs(y[i]) <= 3.4028234663852886e38 ? fmax(top, fabs(y[i])) : INFINITY;
   }
   top = fmax(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = fmax(top, __shfl_xor_sync(0xffffffffu, top, 2));
   const long long b = __double_as_longlong(top);
   const int c = static_cast<int>(b >> 52) - 1023 + 127 - 8 + ((b & 0xFFFFFFFFFFFFFll) > 0xC000000000000ll ? 1 : 0);
-  const uint32_t sc = c < 0 ? 0u : static_cast<uint32_t>(c);
+  const uint32_t sc = isinf(top) ? 0xFFu : c < 0 ? 0u : static_cast<uint32_t>(c);
   const double inv = mx_inv_scale(sc);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {  // to fp32 rounded to odd, so that the rounding to e4m3 is the only one
