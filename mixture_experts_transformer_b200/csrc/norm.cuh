@@ -311,8 +311,21 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rms_norm_kernel(con
       // as near to where the scale changes
       constexpr uint32_t kNear = 4;
       uint32_t off = ((m & 0x7FFFFFu) - 0x600000u + kNear) & 0x7FFFFFu;
+      float least = INFINITY;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) off = min(off, (__float_as_uint(f[i]) - 0x80000u + kNear) & 0xFFFFFu);
+      for (int i = 0; i < 8; ++i) {
+        off = min(off, (__float_as_uint(f[i]) - 0x80000u + kNear) & 0xFFFFFu);
+        least = fminf(least, fabsf(f[i]));
+      }
+      // Below 2^-6 codes are 2^-9 apart, as in the binade from 2^-6 on: 2^-6 more has the middles' bits. At the smallest
+      // scale an fp32 y may hold fewer than 24 bits.
+      if (least < 0.015625f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (fabsf(f[i]) < 0.015625f)
+            off = min(off, (__float_as_uint(fabsf(f[i]) + 0.015625f) - 0x80000u + kNear) & 0xFFFFFu);
+      }
+      if (sc == 0 && m != 0) off = 0;
       if (off <= 2 * kNear) near |= 1u << u;
       if (in) {
         reinterpret_cast<uint2*>(P.q + row)[v] = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
