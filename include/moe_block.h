@@ -533,7 +533,9 @@ moe_status moe_block_forward_few(const moe_params* p, void* stream);
  *   y = gamma s / sqrt(mean(s^2) + eps)
  * per row of [T, embed_dim], in fp32, each output rounded once from there:
  *   sum = RNE_bf16(s), y = RNE_bf16(y), (q, scale) = MXFP8(y).
- * (A code that the fp32 y leaves open is taken from y in 64 bits.)
+ * (A code that the fp32 y leaves open is taken from y in 64 bits, made from x
+ * on; the sum of squares of s is added up in fp32 for eight values at a time,
+ * in 64 bits from there.)
  * residual, gamma_post and gamma (bf16; NULL: no addition, no post-norm, no
  * learned scale) are optional, and so is each output, but one is needed and q
  * comes with scale. embed_dim (0: MOE_EMBED_DIM) is a multiple of 8, of 32 with

@@ -231,6 +231,9 @@ moe_status device_state(DeviceState** out) {
                                kFewMaxSmem - kFewStaticSmem) !=
               cudaSuccess)
         return MOE_ERR_CUDA;
+      if (cudaFuncSetAttribute(add_rms_norm_kernel<512, 4, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               norm_smem(512, 4, true)) != cudaSuccess)  // the only one above the ordinary 48 KB
+        return MOE_ERR_CUDA;
       if (cudaFuncSetAttribute(mx_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmemBytes) !=
               cudaSuccess ||
           cudaFuncSetAttribute(mx_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmemBytes) !=
@@ -1284,9 +1287,10 @@ moe_status enqueue_few_mx(const moe_mxfp8_params* p, const Dims& d, const FewLay
 }
 
 template <int TPR, int NV>
-cudaError_t launch_add_norm(const AddNormParams& P, cudaStream_t st) {
+cudaError_t launch_add_norm(const AddNormParams& P, bool keep, cudaStream_t st) {
   constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
-  return launch_k(add_rms_norm_kernel<TPR, NV>, (P.T + kRows - 1) / kRows, TPR < 128 ? 128 : TPR, 0, st, P);
+  return launch_k(keep ? add_rms_norm_kernel<TPR, NV, true> : add_rms_norm_kernel<TPR, NV, false>,
+                  (P.T + kRows - 1) / kRows, norm_threads(TPR), norm_smem(TPR, NV, keep), st, P);
 }
 
 // -------------------------------------------------- weight-only formats
@@ -2136,6 +2140,8 @@ moe_status moe_add_rms_norm(const moe_norm_params* p, void* stream) {
   DeviceState* s = nullptr;
   MOE_TRY(device_state(&s));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool in_place = p->sum == p->x || p->y == p->x || (p->residual && (p->sum == p->residual || p->y == p->residual));
+  const bool keep = p->q && in_place;
   const AddNormParams P{p->T,
                         D,
                         eps,
@@ -2150,12 +2156,12 @@ moe_status moe_add_rms_norm(const moe_norm_params* p, void* stream) {
                         static_cast<uint8_t*>(p->scale)};
   LaunchScope ls_(kKAddNorm, st);
   const int nvec = D / 8;  // 16-byte vectors of a row
-  return ls_.done(nvec <= 32        ? launch_add_norm<32, 1>(P, st)
-                  : nvec <= 4 * 32  ? launch_add_norm<32, 4>(P, st)
-                  : nvec <= 3 * 128 ? launch_add_norm<128, 3>(P, st)
-                  : nvec <= 4 * 128 ? launch_add_norm<128, 4>(P, st)
-                  : nvec <= 2 * 512 ? launch_add_norm<512, 2>(P, st)
-                                    : launch_add_norm<512, 4>(P, st));
+  return ls_.done(nvec <= 32        ? launch_add_norm<32, 1>(P, keep, st)
+                  : nvec <= 4 * 32  ? launch_add_norm<32, 4>(P, keep, st)
+                  : nvec <= 3 * 128 ? launch_add_norm<128, 3>(P, keep, st)
+                  : nvec <= 4 * 128 ? launch_add_norm<128, 4>(P, keep, st)
+                  : nvec <= 2 * 512 ? launch_add_norm<512, 2>(P, keep, st)
+                                    : launch_add_norm<512, 4>(P, keep, st));
 }
 
 size_t moe_few_workspace_bytes(const moe_params* p) {

@@ -63,12 +63,12 @@ def test_a_gamma_that_is_not_finite_takes_its_group_alone(T, D, bad):
                                   to_np(ref.q.view(torch.uint8)).reshape(T, -1, 32)[:, ~hit])
 
 
-# What 64-bit arithmetic of a row (sums of up to 2^14 squares in order, 2^-53 each, a root, a few products) may leave
-# open: 2^14 2^-53 of the sum at most, so anything within 2^-38 of a border may fall on either side.
-OPEN = 2.0**-38
+# Codes are decided in 64 bits but for the row's sum of squares: of each eight squares at most 5 fp32 roundings, and what
+# s's own (one; after a post-norm two) bring in, twice each: 9 2^-24 of the sum and half of that of y, relatively.
+OPEN = 4.5 * 2.0**-24
 
 
-def check_codes(res, y):
+def check_codes(res, y, open=OPEN):
     """Codes and scales of res are the 64-bit oracle's of y."""
     q, j = mx.quantize(y)
     codes = to_np(res.q.float()).astype(np.float64)
@@ -77,13 +77,13 @@ def check_codes(res, y):
     if other.any():
         amax = np.abs(y).reshape(*j.shape, 32).max(-1)[other]
         top = 448 * np.exp2(np.minimum(scale, j)[other].astype(np.float64))
-        assert np.all(np.abs(amax - top) <= OPEN * top), np.count_nonzero(other)
+        assert np.all(np.abs(amax - top) <= open * top), np.count_nonzero(other)
     w = y / np.exp2(np.repeat(scale, 32, -1).astype(np.float64))
     q = mx.e4m3_round(np.clip(w, -448, 448))
     other = codes != q
     if other.any():
         mid = (codes + q)[other] / 2
-        assert np.all(np.abs(w[other] - mid) <= OPEN * np.abs(mid)), np.count_nonzero(other)
+        assert np.all(np.abs(w[other] - mid) <= open * np.abs(mid)), np.count_nonzero(other)
 
 
 def split(s):
@@ -105,7 +105,10 @@ def test_codes_below_the_normal_range(T, D):
     s[:, :, 7] = (large * rng.choice([-1, 1], (T, D // 32, 1)))[:, :, 0]
     s = s.reshape(T, D)
     xb, rb = split(s)
-    check_codes(run(xb, rb), oracle(xb, rb))
+    # a bf16 square is exact in fp32, and so is the sum of those of one magnitude, at most 2^9 of them; what may be lost
+    # are the small ones: 31 (7.5 2^-9 / 362)^2 of the sum for each large one (362 = 448 2^-7 .. on the scale of 2^-6), 0.42
+    # 2^-24 of y. The large value alone fills a code; the sum's own 5 roundings do not arise.
+    check_codes(run(xb, rb), oracle(xb, rb), open=0.45 * 2.0**-24)
 
 
 def by_the_middles(rng, T, D):
@@ -124,6 +127,63 @@ def by_the_middles(rng, T, D):
 def test_codes_by_the_middles(T, D):
     xb, rb = split(by_the_middles(np.random.default_rng(D + 1), T, D))
     check_codes(run(xb, rb), oracle(xb, rb))
+
+
+@pytest.mark.parametrize("D", [256, 2816, 4096, 16384])
+def test_codes_by_the_middles_after_a_post_norm(D):
+    """The post-norm carries what the residual, in bf16, leaves of s: its gamma is made for the one row."""
+    rng = np.random.default_rng(D + 2)
+    for _ in range(8):
+        s = by_the_middles(rng, 1, D)
+        rb = sw.bf16_bits(sw.bf16_rne(s))
+        xb = bits(rng.uniform(1, 2, (1, D)) * rng.choice([-1, 1], (1, D)))
+        rest = (s - mo.f64(rb)) / sw.rms_norm(mo.f64(xb))
+        pb = sw.bf16_bits(sw.bf16_rne(rest[0]))
+        check_codes(run(xb, rb, None, pb), oracle(xb, rb, None, pb))
+
+
+@pytest.mark.parametrize("T,D", [(700, 2816), (3000, 256), (300, 4096), (64, 16384), (90, 1024), (50, 1056)])
+@pytest.mark.parametrize("post", [False, True])
+def test_codes_of_ordinary_rows(T, D, post):
+    rng = np.random.default_rng(T)
+    xb, rb = bits(rng.standard_normal((T, D))), bits(2 * rng.standard_normal((T, D)))
+    gb = bits(1 + 0.1 * rng.standard_normal(D))
+    pb = bits(1 + 0.1 * rng.standard_normal(D)) if post else None
+    check_codes(run(xb, rb, gb, pb), oracle(xb, rb, gb, pb))
+
+
+@pytest.mark.parametrize("T,D", [(100, 2816), (300, 256), (20, 16384)])
+def test_codes_where_the_residual_cancels(T, D):
+    """residual = -(post-norm of x), rounded to bf16: s is what that rounding left, 2^-9 of either."""
+    rng = np.random.default_rng(T)
+    xb, pb = bits(rng.standard_normal((T, D))), bits(1 + 0.1 * rng.standard_normal(D))
+    rb = sw.bf16_bits(sw.bf16_rne(-sw.rms_norm(mo.f64(xb), mo.f64(pb))))
+    gb = bits(1 + 0.1 * rng.standard_normal(D))
+    res = run(xb, rb, gb, pb)
+    y = oracle(xb, rb, gb, pb)
+    check_codes(res, y)
+    # sum is rounded once, by half of bf16's step of 2^-7 at most, from an s good to a few 2^-24 of itself
+    s = mo.f64(rb) + sw.rms_norm(mo.f64(xb), mo.f64(pb))
+    assert np.all(np.abs(to_np(res.sum.double()) - s) <= (2.0**-8 + 2.0**-21) * np.abs(s) + 2.0**-130)
+
+
+@pytest.mark.parametrize("post", [False, True])
+@pytest.mark.parametrize("T,D", [(900, 256), (400, 2816), (40, 16384)])
+def test_codes_in_place(T, D, post):
+    """With 8-bit output, sum and y over residual and x: everything as in separate buffers."""
+    rng = np.random.default_rng(T)
+    xb, rb = bits(rng.standard_normal((T, D))), bits(2 * rng.standard_normal((T, D)))
+    gb = bits(1 + 0.1 * rng.standard_normal(D))
+    pb = bits(1 + 0.1 * rng.standard_normal(D)) if post else None
+    ref = run(xb, rb, gb, pb)
+    for swap in (False, True):
+        x, r = block.bf16_tensor(xb), block.bf16_tensor(rb)
+        y, s = (r, x) if swap else (x, r)
+        got = block.add_rms_norm(x, block.bf16_tensor(gb), residual=r, quantize=True, y=y, sum_out=s,
+                                 gamma_post=None if pb is None else block.bf16_tensor(pb))
+        ok()
+        for a, b in ((got.y, ref.y), (got.sum, ref.sum), (got.q, ref.q), (got.scale, ref.scale)):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
 @pytest.mark.parametrize("below", [0, 3, 7, 10])
