@@ -320,6 +320,13 @@ def _on_current_device(x: torch.Tensor) -> int:
     return index
 
 
+def _weights_on(device: int, tensors: dict) -> None:
+    """Refuses weights that are not on CUDA device `device` (where the library runs)."""
+    for name, t in tensors.items():
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on {t.device}: the call runs on cuda:{device}")
+
+
 _BF16, _E4M3, _E8M0 = (torch.bfloat16,), (torch.float8_e4m3fn, torch.uint8), (torch.float8_e8m0fnu, torch.uint8)
 
 
@@ -347,6 +354,7 @@ def forward_few(
     dev = _on_current_device(x)
     T, D = x.shape[0], dw.dims.embed_dim
     _rows("x", x, (T, D), _BF16, dev)
+    _weights_on(dev, {n: getattr(dw, n) for n in ("w_router", "wg", "wu", "wd", "sg", "su", "sd")})
     for name, t in (("norm_pre", norm_pre), ("norm_post", norm_post)):
         if t is not None:
             _rows(name, t, (D,), _BF16, dev)
@@ -486,6 +494,12 @@ class Mxfp8Weights:
             lin = getattr(self, name)
             if (lin.groups, lin.K, lin.N) != (G, K, N):
                 raise ValueError(f"{name}: {G} Linears [{K}, {N}] expected, got {lin.groups} of [{lin.K}, {lin.N}]")
+            if lin.q.device != self.w_router.device or lin.sf.device != self.w_router.device:
+                raise ValueError(f"{name}: on {lin.q.device} and {lin.sf.device}, the router on {self.w_router.device}")
+        r = self.w_router
+        if r.shape != (d.embed_dim, d.num_experts) or r.dtype != torch.bfloat16 or not r.is_contiguous():
+            raise ValueError(f"w_router: needs a contiguous {(d.embed_dim, d.num_experts)} tensor of torch.bfloat16, got "
+                             f"{tuple(r.shape)} {r.dtype}, strides {r.stride()}")
 
 
 def quantize_mxfp8(dw: DeviceWeights, stream=None) -> Mxfp8Weights:
@@ -529,6 +543,7 @@ def forward_mxfp8(
     dev = _on_current_device(x)
     T, D = x.shape[0], mw.dims.embed_dim
     _rows("x", x, (T, D), _BF16, dev)
+    _weights_on(dev, {"w_router": mw.w_router})  # (the others are where it is)
     if xq is not None:
         _rows("xq", xq, (T, D), _E4M3, dev)
     if xs is not None:

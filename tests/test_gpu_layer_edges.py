@@ -77,3 +77,26 @@ def test_infinite_logits_choose_as_the_whole_block(T):
             for res in (got, mx):
                 assert torch.equal(res.idx, ref.idx)
                 np.testing.assert_allclose(to_np(res.w), to_np(ref.w), rtol=2e-5, atol=1e-9)
+
+
+# ------------------------------------------------------- where tensors are
+
+
+def test_weights_elsewhere_are_refused():
+    """Weights in host memory: refused before anything is launched."""
+    x = block.bf16_tensor(inputs.make_x(4, SMALL.embed_dim, seed=1))
+    dw = block.upload(weights(SMALL), device="cpu")
+    with pytest.raises(ValueError, match="w_router is on cpu"):
+        block.forward_few(dw, x, top_k=4)
+    for name in ("wg", "sd"):
+        mixed = dataclasses.replace(device_weights(SMALL), **{name: getattr(dw, name)})
+        with pytest.raises(ValueError, match=f"{name} is on cpu"):
+            block.forward_few(mixed, x, top_k=4)
+    mw = block.quantize_mxfp8(device_weights(SMALL))
+    host = [block.Mxfp8Linear(lin.q.cpu(), lin.sf.cpu(), lin.groups, lin.K, lin.N)
+            for lin in (mw.wg, mw.wu, mw.wd, mw.sg, mw.su, mw.sd)]
+    with pytest.raises(ValueError, match="w_router is on cpu"):
+        block.forward_mxfp8(block.Mxfp8Weights(mw.dims, mw.w_router.cpu(), *host), x, top_k=4)
+    with pytest.raises(ValueError, match="wg: on cpu"):
+        block.Mxfp8Weights(mw.dims, mw.w_router, *host)
+    ok()
