@@ -320,6 +320,17 @@ def _on_current_device(x: torch.Tensor) -> int:
     return index
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory that `stream` (None: the current one) is to write: from that stream's pool, as other streams may still be
+    using what the current one's holds, and not to be taken for another tensor while the current stream reads it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def _weights_on(device: int, tensors: dict) -> None:
     """Refuses weights that are not on CUDA device `device` (where the library runs)."""
     for name, t in tensors.items():
@@ -363,11 +374,11 @@ def forward_few(
     if workspace is not None:
         _rows("workspace", workspace, workspace.shape, (torch.uint8,), dev)
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty((T, D), torch.bfloat16, x.device, stream)
     _rows("out", out, (T, D), _BF16, dev)
-    res = _result(out, dw.dims, top_k, debug)
+    res = _result(out, dw.dims, top_k, debug, stream)
     if debug:
-        res.logits = torch.empty((T, dw.dims.num_experts), dtype=torch.float32, device=x.device)
+        res.logits = _empty((T, dw.dims.num_experts), torch.float32, x.device, stream)
     d, ptr = dw.dims, B.ptr
     p = B.MoeParams(T, top_k, D, d.num_experts, d.expert_dim, d.hidden_dim, ptr(x), ptr(dw.w_router), ptr(router_bias),
                     ptr(dw.wg), ptr(dw.wu), ptr(dw.wd), ptr(dw.sg), ptr(dw.su), ptr(dw.sd), ptr(out), ptr(res.out_f32),
@@ -414,16 +425,16 @@ def add_rms_norm(
     pgam = None if gamma is None else _rows("gamma", gamma, (D,), _BF16, dev)
     ppost = None if gamma_post is None else _rows("gamma_post", gamma_post, (D,), _BF16, dev)
     if y is None:
-        y = torch.empty_like(x)
+        y = _empty(shape, torch.bfloat16, x.device, stream)
     if sum_out is None:
-        sum_out = torch.empty_like(x)
+        sum_out = _empty(shape, torch.bfloat16, x.device, stream)
     py, psum = _rows("y", y, shape, _BF16, dev), _rows("sum_out", sum_out, shape, _BF16, dev)
     pq = pscale = None
     if quantize or q is not None or scale is not None:
         if q is None:
-            q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
+            q = _empty(shape, torch.float8_e4m3fn, x.device, stream)
         if scale is None:
-            scale = torch.empty((T, D // B.MXFP8_GROUP), dtype=torch.float8_e8m0fnu, device=x.device)
+            scale = _empty((T, D // B.MXFP8_GROUP), torch.float8_e8m0fnu, x.device, stream)
         pq = _rows("q", q, shape, _E4M3, dev)
         pscale = _rows("scale", scale, (T, D // B.MXFP8_GROUP), _E8M0, dev)
     p = B.MoeNormParams(T, D, eps, px, pres, ppost, pgam, psum, py, pq, pscale)
@@ -458,8 +469,8 @@ def quantize_mxfp8_linear(w: torch.Tensor, stream=None) -> Mxfp8Linear:
     G, K, N = w3.shape
     _rows("w", w3, (G, K, N), _BF16, _on_current_device(w3))
     _, sfb = B.moe_mxfp8_weight_bytes(G, K, N)
-    q = torch.empty((G, N, K), dtype=torch.float8_e4m3fn, device=w.device)
-    sf = torch.empty(sfb, dtype=torch.float8_e8m0fnu, device=w.device)
+    q = _empty((G, N, K), torch.float8_e4m3fn, w.device, stream)
+    sf = _empty(sfb, torch.float8_e8m0fnu, w.device, stream)
     B.check(B.moe_mxfp8_quantize_weight(w3, G, K, N, q, sf, stream), "moe_mxfp8_quantize_weight")
     return Mxfp8Linear(q, sf, G, K, N)
 
@@ -469,8 +480,8 @@ def quantize_mxfp8_rows(x: torch.Tensor, stream=None) -> tuple[torch.Tensor, tor
     T, D = x.shape
     dev = _on_current_device(x)
     _rows("x", x, (T, D), _BF16, dev)
-    q = torch.empty((T, D), dtype=torch.float8_e4m3fn, device=x.device)
-    scale = torch.empty((T, D // B.MXFP8_GROUP), dtype=torch.float8_e8m0fnu, device=x.device)
+    q = _empty((T, D), torch.float8_e4m3fn, x.device, stream)
+    scale = _empty((T, D // B.MXFP8_GROUP), torch.float8_e8m0fnu, x.device, stream)
     B.check(B.moe_mxfp8_quantize_act(x, T, D, q, scale, stream), "moe_mxfp8_quantize_act")
     return q, scale
 
@@ -553,22 +564,22 @@ def forward_mxfp8(
     if workspace is not None:
         _rows("workspace", workspace, workspace.shape, (torch.uint8,), dev)
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty((T, D), torch.bfloat16, x.device, stream)
     _rows("out", out, (T, D), _BF16, dev)
-    res = _result(out, mw.dims, top_k, debug)
+    res = _result(out, mw.dims, top_k, debug, stream)
     p = mxfp8_params(mw, T, x, out, xq=xq, xs=xs, top_k=top_k, router_bias=router_bias, res=res, workspace=workspace)
     B.check(B.moe_block_forward_mxfp8(p, stream), "moe_block_forward_mxfp8")
     return res
 
 
-def _result(out: torch.Tensor, dims: Dims, top_k: int, debug: bool) -> BlockResult:
+def _result(out: torch.Tensor, dims: Dims, top_k: int, debug: bool, stream) -> BlockResult:
     res = BlockResult(out=out)
     if debug:
         T, dev = out.shape[0], out.device
-        res.out_f32 = torch.empty((T, dims.embed_dim), dtype=torch.float32, device=dev)
-        res.idx = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-        res.w = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-        res.cnt = torch.empty((dims.num_experts,), dtype=torch.int32, device=dev)
+        res.out_f32 = _empty((T, dims.embed_dim), torch.float32, dev, stream)
+        res.idx = _empty((T, top_k), torch.int32, dev, stream)
+        res.w = _empty((T, top_k), torch.float32, dev, stream)
+        res.cnt = _empty((dims.num_experts,), torch.int32, dev, stream)
     return res
 
 

@@ -100,3 +100,67 @@ def test_weights_elsewhere_are_refused():
     with pytest.raises(ValueError, match="wg: on cpu"):
         block.Mxfp8Weights(mw.dims, mw.w_router, *host)
     ok()
+
+
+def _calls(T):
+    """name -> (call(stream) -> result tensors): everything that makes its own outputs."""
+    dw = device_weights(SMALL)
+    mw = block.quantize_mxfp8(dw)
+    x = block.bf16_tensor(inputs.make_x(T, SMALL.embed_dim, seed=T))
+    wf, wm = block.few_workspace(dw, min(T, 16), 4), block.mxfp8_workspace(mw, T, 4)
+
+    def norm(st):
+        r = block.add_rms_norm(x, residual=x, quantize=True, stream=st)
+        return r.y, r.sum, r.q, r.scale
+
+    def linear(st):
+        lin = block.quantize_mxfp8_linear(dw.sg, stream=st)
+        return lin.q, lin.sf
+
+    def layer(r):
+        return r.out, r.out_f32, r.idx, r.w, r.cnt
+
+    calls = {
+        "norm": norm,
+        "rows": lambda st: block.quantize_mxfp8_rows(x, stream=st),
+        "linear": linear,
+        "mxfp8": lambda st: layer(block.forward_mxfp8(mw, x, top_k=4, workspace=wm, stream=st, debug=True)),
+    }
+    if T <= 16:
+        calls["few"] = lambda st: layer(block.forward_few(dw, x, top_k=4, workspace=wf, stream=st, debug=True))
+    return calls
+
+
+@pytest.mark.parametrize("T", [7, 40])
+def test_outputs_of_a_call_on_another_stream(T):
+    """A call given a stream makes its outputs from memory that the current stream no longer writes, and a later call's
+    outputs do not take memory that the current stream still reads."""
+    calls = _calls(T)
+    side = torch.cuda.Stream()
+    for name, call in calls.items():
+        ref = [t.clone() for t in call(None)]
+        ok()
+        torch.cuda.synchronize()
+        # freed here, but to be written by this stream some 10 ms from now
+        old = [torch.empty_like(t) for t in ref]
+        torch.cuda._sleep(20_000_000)
+        for t in old:
+            t.view(torch.uint8).fill_(7)
+        del old, t
+        got = call(side)
+        torch.cuda.synchronize()
+        ok()
+        for a, b in zip(got, ref):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), name
+        # read by this stream some 10 ms from now, but freed at once
+        torch.cuda._sleep(20_000_000)
+        kept = [t.clone() for t in got]
+        del got, a
+        again = call(side)
+        with torch.cuda.stream(side):
+            for t in again:
+                t.view(torch.uint8).fill_(9)
+        torch.cuda.synchronize()
+        for a, b in zip(kept, ref):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), name
+        del again, t, a, b
