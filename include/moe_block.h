@@ -580,7 +580,8 @@ moe_status moe_mxfp8_quantize_act(const void* x, int rows, int K, uint8_t* q, ui
  *   rows; products of 8-bit values, fp32 accumulation. The router reads x in
  *   bf16 (top-k and weights as in the bf16 block).
  * xq / xs (both or neither): the rows x already in MXFP8, e.g. as
- * moe_add_rms_norm wrote them beside x; without them the call quantises x.
+ * moe_add_rms_norm wrote them beside x, each 16-byte aligned; without them the
+ * call quantises x.
  * Dims, w_router, router_bias, out, out_f32, idx_out, w_out, cnt_out as in
  * moe_params; out may be NULL when out_f32 is given. Outputs must not overlap
  * x, xq, xs or one another. workspace: at least moe_mxfp8_workspace_bytes(p),

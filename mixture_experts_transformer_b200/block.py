@@ -550,15 +550,18 @@ def forward_mxfp8(
 ) -> BlockResult:
     """One block with MXFP8 weights and activations. x [T, D] bf16 feeds the
     router; xq / xs are the same rows in MXFP8 (as add_rms_norm writes them),
-    without them the call quantises x."""
+    without them the call quantises x. (xs off a 16-byte boundary, as a slice of
+    a batch's rows may be, is copied to one first.)"""
     dev = _on_current_device(x)
     T, D = x.shape[0], mw.dims.embed_dim
     _rows("x", x, (T, D), _BF16, dev)
     _weights_on(dev, {"w_router": mw.w_router})  # (the others are where it is)
     if xq is not None:
         _rows("xq", xq, (T, D), _E4M3, dev)
-    if xs is not None:
-        _rows("xs", xs, (T, D // B.MXFP8_GROUP), _E8M0, dev)
+    if xs is not None and _rows("xs", xs, (T, D // B.MXFP8_GROUP), _E8M0, dev) % 16:
+        xs, part = _empty(xs.shape, xs.dtype, xs.device, stream), xs  # (rows of a batch may start anywhere)
+        with torch.cuda.stream(stream):
+            xs.view(torch.uint8).copy_(part.view(torch.uint8))
     if router_bias is not None:
         _rows("router_bias", router_bias, (mw.dims.num_experts,), (torch.float32,), dev)
     if workspace is not None:

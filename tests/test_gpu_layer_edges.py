@@ -164,3 +164,41 @@ def test_outputs_of_a_call_on_another_stream(T):
         for a, b in zip(kept, ref):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), name
         del again, t, a, b
+
+
+@pytest.mark.parametrize("T", [3, 40])
+def test_scales_of_a_slice_of_rows(T):
+    """Rows of one batch whose scales start off a 16-byte boundary (embed 320: 10 bytes a row), on the current and on
+    another stream, and in a captured graph."""
+    dims = inputs.Dims(embed_dim=320, num_experts=24, expert_dim=64, hidden_dim=448)
+    mw = block.quantize_mxfp8(device_weights(dims))
+    x = block.bf16_tensor(inputs.make_x(T + 5, 320, seed=T))
+    xq, xs = block.quantize_mxfp8_rows(x)
+    ws = block.mxfp8_workspace(mw, T, 4)
+    side = torch.cuda.Stream()
+    for first in (1, 3, 5):
+        rows = slice(first, first + T)
+        assert xs[rows].data_ptr() % 16
+        ref = block.forward_mxfp8(mw, x[rows], xq=xq[rows], xs=xs[rows].clone(), top_k=4).out
+        got = block.forward_mxfp8(mw, x[rows], xq=xq[rows], xs=xs[rows], top_k=4).out
+        ok()
+        assert torch.equal(got, ref)
+        torch.cuda.synchronize()
+        got = block.forward_mxfp8(mw, x[rows], xq=xq[rows], xs=xs[rows], top_k=4, workspace=ws, stream=side).out
+        torch.cuda.synchronize()
+        assert torch.equal(got, ref)
+    out = torch.zeros_like(ref)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        block.forward_mxfp8(mw, x[rows], xq=xq[rows], xs=xs[rows], top_k=4, workspace=ws, out=out)
+    new = block.bf16_tensor(inputs.make_x(T + 5, 320, seed=T + 1))
+    x.copy_(new)
+    for a, b in zip((xq, xs), block.quantize_mxfp8_rows(new)):
+        a.view(torch.uint8).copy_(b.view(torch.uint8))
+    ref = block.forward_mxfp8(mw, x[rows], xq=xq[rows], xs=xs[rows].clone(), top_k=4).out
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    ok()
+    assert torch.equal(out, ref)
+    del g
