@@ -145,9 +145,13 @@ def stream_handle(stream=None) -> int | None:
         import torch
 
         torch.cuda.current_stream()  # (initialises CUDA)
-        _raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
-    device, raw = _raw_stream
-    return raw(device())
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # (1 us quicker than current_stream(), but internal)
+        if raw is None:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        else:
+            device = torch.cuda.current_device
+            _raw_stream = lambda: raw(device())  # noqa: E731
+    return _raw_stream()
 
 
 def make_params(

@@ -52,3 +52,17 @@ def test_weights_on_another_device_are_refused():
     with pytest.raises(ValueError, match="w_router is on cpu"):
         block._weights_on(0, {"w_router": router})
     block._weights_on(-1, {"w_router": router})
+
+
+def test_stream_handle_without_the_raw_stream_call(monkeypatch):
+    """The handle of the current stream comes through torch's public call where the quicker internal one is missing."""
+
+    class Stream:
+        cuda_stream = 1234
+
+    monkeypatch.setattr(B, "_raw_stream", None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream)
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    assert B.stream_handle() == 1234
+    assert B.stream_handle() == 1234
+    assert B.stream_handle(Stream) == 1234
