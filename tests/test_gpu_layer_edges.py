@@ -9,6 +9,8 @@ import torch
 from gpu_common import SMALL, device_weights, require_gpu, to_np, weights
 from mixture_experts_transformer_b200 import binding as B
 from mixture_experts_transformer_b200 import block, inputs
+from test_gpu_few import check
+from test_gpu_mxfp8 import check_block
 
 pytestmark = pytest.mark.gpu
 
@@ -202,3 +204,156 @@ def test_scales_of_a_slice_of_rows(T):
     ok()
     assert torch.equal(out, ref)
     del g
+
+
+# ------------------------------------------------------------------ limits
+
+
+@pytest.mark.parametrize("S", [16320, 16384])
+@pytest.mark.parametrize("T", [1, 16])
+def test_few_with_the_widest_shared_mlp(S, T):
+    """16384 hidden units of the shared MLP: 128 units of work, a CTA has parts of two at most."""
+    dims = inputs.Dims(embed_dim=128, num_experts=8, expert_dim=64, hidden_dim=S)
+    w, dw = weights(dims), device_weights(dims)
+    xb = inputs.make_x(T, 128, seed=T)
+    res = block.forward_few(dw, block.bf16_tensor(xb), top_k=2, debug=True)
+    ok()
+    assert B.moe_last_launch_count() == 2
+    check(w, xb, res, 2)
+    res = block.forward_mxfp8(block.quantize_mxfp8(dw), block.bf16_tensor(xb), top_k=2, debug=True)
+    ok()
+    assert B.moe_last_launch_count() == 2
+    check_block(w, xb, res, 2)
+
+
+@pytest.mark.parametrize("E,T", [(32, 1), (32, 16), (40, 1), (128, 16)])
+def test_few_with_the_most_choices(E, T):
+    """top_k 32, a warp's worth of slots: of 32 experts (all), 40 and 128."""
+    dims = inputs.Dims(embed_dim=192, num_experts=E, expert_dim=64, hidden_dim=64)
+    w, dw = weights(dims), device_weights(dims)
+    xb = inputs.make_x(T, 192, seed=E + T)
+    res = block.forward_few(dw, block.bf16_tensor(xb), top_k=32, debug=True)
+    ok()
+    check(w, xb, res, 32)
+    res = block.forward_mxfp8(block.quantize_mxfp8(dw), block.bf16_tensor(xb), top_k=32, debug=True)
+    ok()
+    assert B.moe_last_launch_count() == 2
+    check_block(w, xb, res, 32)
+
+
+@pytest.mark.parametrize("T", [1, 16])
+def test_few_with_the_widest_experts(T):
+    dims = inputs.Dims(embed_dim=64, num_experts=8, expert_dim=16384, hidden_dim=64)
+    w, dw = weights(dims), device_weights(dims)
+    xb = inputs.make_x(T, 64, seed=T)
+    res = block.forward_few(dw, block.bf16_tensor(xb), top_k=3, debug=True)
+    ok()
+    check(w, xb, res, 3)
+    res = block.forward_mxfp8(block.quantize_mxfp8(dw), block.bf16_tensor(xb), top_k=3, debug=True)
+    ok()
+    assert B.moe_last_launch_count() == 2
+    check_block(w, xb, res, 3)
+
+
+@pytest.mark.parametrize("T", [1, 16, 17])
+@pytest.mark.parametrize("D,F,S", [(4160, 64, 64), (128, 64, 16448), (64, 16448, 64)])
+def test_past_the_few_token_forms_limits(T, D, F, S):
+    """Wider than the few-token form holds: MXFP8 calls take the grouped GEMMs at any size, bf16 calls are refused."""
+    dims = inputs.Dims(embed_dim=D, num_experts=8, expert_dim=F, hidden_dim=S)
+    w, dw = weights(dims), device_weights(dims)
+    xb = inputs.make_x(T, D, seed=T)
+    x = block.bf16_tensor(xb)
+    mw = block.quantize_mxfp8(dw)
+    res = block.forward_mxfp8(mw, x, top_k=2, debug=True, workspace=block.mxfp8_workspace(mw, 40, 2))
+    ok()
+    assert B.moe_last_launch_count() > 2
+    check_block(w, xb, res, 2)
+    with pytest.raises(B.MoeError) as err:
+        block.forward_few(dw, x, top_k=2)
+    assert err.value.status == B.MOE_ERR_INVALID_ARG
+    p = B.make_params(T, top_k=2, dims=dims)
+    assert B.moe_few_workspace_bytes(p) == 0
+
+
+# ------------------------------------------- the grouped form, in earnest
+
+
+@pytest.mark.parametrize("T", [17, 40, 300])
+def test_grouped_special_values_stay_with_their_tokens(T):
+    """More than 16 tokens: a NaN and an infinite row touch their own output alone, bad weights of an expert the tokens
+    routed to it alone."""
+    w, dw = weights(SMALL), device_weights(SMALL)
+    mw = block.quantize_mxfp8(dw)
+    x = block.bf16_tensor(inputs.make_x(T, SMALL.embed_dim, seed=T))
+    ref = block.forward_mxfp8(mw, x, top_k=2, debug=True)
+    x2 = x.clone()
+    x2[4, 7], x2[T - 1, 255], x2[9] = float("nan"), float("inf"), float("-inf")
+    got = block.forward_mxfp8(mw, x2, top_k=2, debug=True)
+    ok()
+    bad = torch.zeros(T, dtype=torch.bool, device="cuda")
+    bad[[4, 9, T - 1]] = True
+    assert torch.isnan(got.out_f32[bad]).all() and torch.equal(got.out_f32[~bad], ref.out_f32[~bad])
+    assert all(len(set(r)) == 2 for r in to_np(got.idx))
+    e = int(ref.idx[0, 0])
+    arrays = [a.copy() for a in (w.wg, w.wu, w.wd)]
+    arrays[0][e, 3, 5] = 0x7F80
+    arrays[1][e, 100, 6] = 0xFFC0
+    arrays[2][e, 2, 1] = 0x7FC0
+    mwb = block.quantize_mxfp8(block.upload(dataclasses.replace(w, wg=arrays[0], wu=arrays[1], wd=arrays[2])))
+    got = block.forward_mxfp8(mwb, x, top_k=2, debug=True)
+    ok()
+    hit = (ref.idx == e).any(1)
+    assert hit.any() and not hit.all()
+    assert not torch.isfinite(got.out_f32[hit]).all(1).any() and torch.equal(got.out_f32[~hit], ref.out_f32[~hit])
+
+
+def test_grouped_graphs_and_streams_at_once():
+    """Two captured graphs of different batches on workspaces of their own, replayed on two streams at once, with new
+    inputs each time."""
+    mw = block.quantize_mxfp8(device_weights(SMALL))
+    sizes = (40, 700)
+    xs = [block.bf16_tensor(inputs.make_x(T, SMALL.embed_dim, seed=T)) for T in sizes]
+    outs = [torch.empty_like(x) for x in xs]
+    wss = [block.mxfp8_workspace(mw, T, 4) for T in sizes]
+    streams = [torch.cuda.Stream() for _ in sizes]
+    torch.cuda.synchronize()
+    graphs = []
+    for x, o, ws, st in zip(xs, outs, wss, streams):
+        block.forward_mxfp8(mw, x, top_k=4, out=o, workspace=ws, stream=st)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            for _ in range(3):
+                block.forward_mxfp8(mw, x, top_k=4, out=o, workspace=ws)
+        graphs.append(g)
+    for rnd in range(3):
+        new = [block.bf16_tensor(inputs.make_x(T, SMALL.embed_dim, seed=50 * rnd + T)) for T in sizes]
+        refs = [block.forward_mxfp8(mw, n, top_k=4).out.clone() for n in new]
+        for x, n in zip(xs, new):
+            x.copy_(n)
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for g, st in zip(graphs, streams):
+                with torch.cuda.stream(st):
+                    g.replay()
+        torch.cuda.synchronize()
+        ok()
+        for o, r in zip(outs, refs):
+            assert torch.equal(o, r)
+    del graphs, g
+
+
+def test_grouped_rows_behind_the_batch_and_what_the_workspace_held():
+    """Ragged batches write their own rows, whatever the workspace held before."""
+    mw = block.quantize_mxfp8(device_weights(SMALL))
+    for T in (17, 129, 500):
+        x = block.bf16_tensor(inputs.make_x(T, SMALL.embed_dim, seed=T))
+        same = []
+        for fill in (0.0, float("nan")):
+            buf = torch.full((T + 2, SMALL.embed_dim), 7.0, dtype=torch.bfloat16, device="cuda")
+            ws = torch.full((block.mxfp8_workspace(mw, T, 3).numel() // 4,), fill, device="cuda").view(torch.uint8)
+            block.forward_mxfp8(mw, x, top_k=3, out=buf[:T], workspace=ws)
+            ok()
+            assert torch.all(buf[T:] == 7.0)
+            same.append(buf[:T].clone())
+        assert torch.equal(same[0], same[1]) and torch.isfinite(same[0]).all()
