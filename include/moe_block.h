@@ -590,7 +590,8 @@ moe_status moe_mxfp8_quantize_act(const void* x, int rows, int K, uint8_t* q, ui
  * cached allocation may be freed to grow while the graph still lives). At most
  * MOE_FEW_MAX_TOKENS tokens (with the other limits of moe_block_forward_few)
  * run in that form, more as grouped GEMMs. A workspace of T tokens serves
- * every smaller batch too.
+ * every smaller batch too. Calls that may run at the same time need a workspace
+ * each.
  */
 typedef struct moe_mxfp8_params {
   int T;
@@ -664,7 +665,8 @@ moe_status moe_round_bf16(const float* in, void* out, size_t n, void* stream);
 /*
  * Check the guard words of the caller workspace p->workspace (laid out for
  * p's dims) on their own: MOE_ERR_GUARD from the next moe_get_device_status
- * if they differ from the pattern a guarded call wrote.
+ * if they differ from the pattern a guarded call wrote. (A workspace of
+ * moe_block_forward_few is laid out otherwise: its own call checks its guard.)
  */
 moe_status moe_workspace_guard_check(const moe_params* p, void* stream);
 

@@ -14,9 +14,10 @@
 //     falls inside an output column's reduction; CTAs that share a column
 //     leave fp32 partial sums, and the last of them adds them up in CTA order;
 //   * producer threads keep a ring of TMA copies full across the phases: the
-//     shared MLP's chunks need no routing, so they stream while the small kernel
-//     runs and the experts are chosen, and the first down chunks are already in
-//     flight while the last GeGLU rows are being finished elsewhere.
+//     shared MLP's chunks need no routing, so they stream while the experts are
+//     chosen, and the first down chunks are already in flight while the last
+//     GeGLU rows are being finished elsewhere. (They start when the small kernel
+//     has ended: the barrier behind this kernel's wait for it holds every warp.)
 //
 // Phases (chunk lists): S the shared MLP's gate|up, E the touched experts'
 // gate|up, D all down projections: for each 256 output columns the shared MLP's
@@ -36,8 +37,9 @@
 // expert reaches other tokens).
 //
 // Measured (embed 2816, 128 experts of 704, top-8, shared 2112; of the measured copy rate): bf16 T = 1 45 us (45%),
-// 5 with norms 106 us (66%), 16 173-187 us (83-90%: 972 MB from HBM); MXFP8 T = 1 37 us, 8 70 us (73%). What does not
-// stream is fixed: the small kernel and the gap to this one 6 us, the hand-over to D 7 us, the output 4 us.
+// 5 with norms 106 us (66%), 16 173-187 us (83-90%: 972 MB from HBM); MXFP8 T = 1 37 us, 8 70 us (73%). Outside the
+// stream: the small kernel and the gap to this one 6 us, the hand-over to D 7 us (every CTA waits for all GeGLU rows, also
+// those of sources that it does not read next), the output 4 us.
 //
 // Numerics: fp32 accumulation. bf16 form: the GeGLU rows enter the down product as
 // the sum of two bf16 values (hi + lo, 16 bits of mantissa), the routed sums are
@@ -443,7 +445,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     tmem_alloc(tmem_slot, kFewTmemCols);
     tmem_relinquish();
   }
-  // The kernel may start while few_prep_kernel runs: only the weight copies (threads 0 .. 3) go ahead of its end.
+  // The kernel may be set up while few_prep_kernel runs (barriers, TMEM); the __syncthreads() below holds the copying
+  // warps too until that one has ended.
   if (warp >= kFewProdWarps) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (threadIdx.x <= grid) sBegS[threadIdx.x] = FewSplit(su * ck, grid).begin(threadIdx.x);
   tc_fence_before_sync();

@@ -32,12 +32,6 @@ __device__ __forceinline__ float mx_inv_scale(uint32_t code) {
   return code == 0xFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float((254u - code) << 23);
 }
 
-// 2^(code - 127) (NaN for 0xFF; code 0 is the subnormal 2^-127).
-__device__ __forceinline__ float mx_scale_value(uint32_t code) {
-  return code == 0xFFu ? __uint_as_float(0x7FC00000u) : code == 0u ? __uint_as_float(0x00400000u)
-                                                                   : __uint_as_float(code << 23);
-}
-
 // Four e4m3 codes, v0 in the low byte. NaN gives 0x7F (the sign of a NaN is not kept).
 __device__ __forceinline__ uint32_t e4m3x4(float v0, float v1, float v2, float v3) {
   uint32_t r;
@@ -74,7 +68,11 @@ __device__ __forceinline__ uint32_t mx_group(const float (&v)[32], uint4 (&codes
   return sc;
 }
 
-// GELU, tanh form, to fp32 accuracy: z/2 (1 + tanh(u)) = z / (1 + exp(-2u)).
+// GELU, tanh form, in fp32: z/2 (1 + tanh(u)) = z / (1 + exp(-2u)). Its
+// relative error is at most (4.2 |2u| + 5) 2^-23: six roundings of 2u, each
+// |2u| 2^-24 in the exponent, __expf's 2 + 1.173 |2u| units, __fdividef's two,
+// one more of the sum - 2^-19 at |z| = 1, 2^-17 at z = -4, where the value is
+// 1e-4 of z. (1 + tanh(u) in fp32 loses all of its bits there.)
 // The MXFP8 quantiser behind it turns an error d of a value into a flipped
 // code with probability d / step, so the approximate tanh (absolute error
 // 2^-11) would cost up to 2^-11-sized flips of whole e4m3 steps.

@@ -94,7 +94,7 @@ __global__ void mx_act_quant_kernel(const __nv_bfloat16* __restrict__ x, size_t 
 // MLP reads in place - the token-order codes. The blocks of a grid column (y) take
 // every gridDim.y-th 32 groups: with one warp for a whole row too few loads were in
 // flight. A store instruction of the warp covers 512 contiguous bytes of a row (each lane storing its own two pieces
-// left half of every sector to the next instruction: T = 4096 35 us; now 26 us for 115 MB, 68% of the copy rate).
+// left half of every sector to the next instruction: T = 4096 35 us; now 26 us for 130 MB, 76% of the copy rate).
 __global__ void __launch_bounds__(256) route_scatter_mx_kernel(
     const int32_t* __restrict__ idx, const uint32_t* __restrict__ masks, const int32_t* __restrict__ base, int T,
     int k, int E, int D, const __nv_bfloat16* __restrict__ x, const uint8_t* __restrict__ xq,
@@ -266,7 +266,10 @@ __device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t saddr) {
 }
 
 // What an epilogue warp does with its 32 rows (rows_valid of them, from row on) of a tile's accumulator, a row a thread:
-// GeGLU and MXFP8 codes, or output rows through the warp's staging buffer (whole-sector stores in row order).
+// GeGLU and MXFP8 codes, or output rows through the warp's staging buffer (whole-sector stores in row order). Routed rows
+// are rounded to bf16 for the combine, as in the bf16 block: in fp32 they would add 185 MB written and as much read at T =
+// 4096, 56 us of 490 at the copy rate, for an error of 0.0017 of the output that is nearly all its own rounding to bf16
+// (0.00173 -> 0.00177). The shared rows stay fp32.
 template <bool GATEUP>
 __device__ __forceinline__ void mx_epilogue(const MxProblem& pr, uint32_t (&acc)[4][32], int rows_valid, int row, int n0,
                                             int wn, int half, int lane, uint8_t* stg) {
@@ -311,9 +314,6 @@ __device__ __forceinline__ void mx_epilogue(const MxProblem& pr, uint32_t (&acc)
   }
 }
 
-// TMEM columns [0, 256): the accumulator (GATEUP: gate 0..127, up 128..255;
-// DOWN: output columns n0 .. n0+255); from 256: one scale slot per stage, A
-// scales at +0, B block 0 at +4, B block 1 at +8.
 // A value that is the same in all lanes, marked so for the compiler: what it computes from such values it keeps in
 // uniform registers, which is where the tensor instructions take their operands from.
 __device__ __forceinline__ int warp_uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
@@ -323,6 +323,9 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
+// TMEM columns [0, 256): the accumulator (GATEUP: gate 0..127, up 128..255;
+// DOWN: output columns n0 .. n0+255); from 256: one scale slot per stage, A
+// scales at +0, B block 0 at +4, B block 1 at +8.
 template <bool GATEUP>
 __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_constant__ MxParams P) {
   extern __shared__ uint8_t smem_raw[];
