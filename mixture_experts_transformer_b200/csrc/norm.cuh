@@ -364,9 +364,10 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_blocks(TPR, NV)) add_r
       };
       const float inv = mx_inv_scale(sc);
       const uint2 codes = codes_of(inv * (1.f + d)), other = codes_of(inv * (1.f - d));
-      // or a maximum as near to where the scale changes, or the smallest scale, where an fp32 y may hold fewer bits
+      // or a maximum as near to where the scale changes, or one of the smallest scales, where an fp32 y may hold fewer bits
+      // of a value that is not rounded to zero (24 bits of 2^-10 2^(sc - 127) end at 2^-149 for sc = 11)
       if (codes.x != other.x || codes.y != other.y || ((m & 0x7FFFFFu) - 0x600000u + off) <= 2 * off ||
-          (sc == 0 && m != 0))
+          (sc < 11 && m != 0))
         near |= 1u << u;
       if (in) {
         reinterpret_cast<uint2*>(P.q + row)[v] = codes;

@@ -211,3 +211,49 @@ def test_codes_of_tiny_rows():
     gb = bits(np.exp2(rng.integers(-120, 1, D).astype(np.float64)))
     ub = bits(rng.standard_normal((T, D)))
     check_codes(run(ub, None, gb), oracle(ub, None, gb))
+
+
+@pytest.mark.parametrize("above", [1, 2, 4, 8, 12])
+def test_codes_of_values_that_fp32_holds_in_part(above):
+    """Groups at the scales just above the smallest: their smaller values lie where fp32 holds fewer than 24 bits."""
+    rng = np.random.default_rng(above)
+    D = 2816
+    for _ in range(8):
+        xb, rb = split(by_the_middles(rng, 1, D))
+        _, j = mx.quantize(oracle(xb, rb))
+        gb = bits(np.full(D, 2.0 ** (-127 + above - int(j.min()))))
+        res = run(xb, rb, gb)
+        assert int(res.scale.view(torch.uint8).min()) == above
+        check_codes(res, oracle(xb, rb, gb))
+
+
+@pytest.mark.parametrize("D", [256, 2816, 4096, 16384])
+def test_post_norm_of_special_rows(D):
+    """Rows with an infinity (x / inf = 0, inf / inf = NaN), a NaN (all NaN), the largest and the smallest values, zeros."""
+    rng = np.random.default_rng(D)
+    T = 6
+    xb, rb = bits(rng.standard_normal((T, D))), bits(rng.standard_normal((T, D)))
+    pb, gb = bits(1 + 0.1 * rng.standard_normal(D)), bits(1 + 0.1 * rng.standard_normal(D))
+    x, r = block.bf16_tensor(xb), block.bf16_tensor(rb)
+    x[0, 7], x[1, 9] = float("-inf"), float("nan")
+    x[2] *= 2.0**100  # squares far past fp32
+    x[3] *= 2.0**-60
+    x[4] = 0.0
+    for kw in ({}, {"y": x.clone(), "sum_out": None}):
+        src = kw.get("y", x)
+        res = block.add_rms_norm(src, block.bf16_tensor(gb), residual=r, gamma_post=block.bf16_tensor(pb), quantize=True, **kw)
+        ok()
+        keep = torch.ones(D, dtype=torch.bool, device="cuda")
+        keep[7] = False
+        assert torch.equal(res.sum[0, keep], r[0, keep]) and torch.isnan(res.sum[0, 7])
+        assert torch.isnan(res.sum[1]).all()
+        for t in (0, 1):
+            assert torch.isnan(res.y[t]).all() and torch.all(res.scale[t].view(torch.uint8) == 0xFF)
+            assert torch.isnan(res.q[t].float()).all()
+        finite = [2, 3, 4, 5]
+        xv = xb.copy()
+        xv[2], xv[3], xv[4] = sw.bf16_bits(mo.f64(xb[2]) * 2.0**100), sw.bf16_bits(mo.f64(xb[3]) * 2.0**-60), 0
+        y = oracle(xv[finite], rb[finite], gb, pb)
+        part = block.NormResult(None, None, res.q[finite], res.scale[finite])
+        check_codes(part, y)
+        assert np.all(np.abs(to_np(res.y[finite].double()) - y) <= (2.0**-8 + 2.0**-20) * np.abs(y))
