@@ -498,11 +498,12 @@ moe_status moe_block_forward_wq(const moe_wq_params* p, void* stream);
  * parameters - norms, residual, expert shards, optional outputs - and the same definition,
  * but nothing between x (after norm_pre) and the output is rounded to bf16, so
  * results differ from moe_block_forward_ex's within its rounding. A router
- * logit that is NaN counts as -infinity, there and here. Bitwise deterministic. workspace: at least moe_few_workspace_bytes(p) bytes, 256-byte
- * aligned, or NULL for the library's cached allocation - but not while the
- * stream is being captured, where NULL returns MOE_ERR_WORKSPACE. The second
- * kernel is launched cooperatively (one CTA per SM, all resident). Calls that may run at
- * the same time need a workspace each.
+ * logit that is NaN counts as -infinity, there and here. Bitwise deterministic.
+ * workspace: at least moe_few_workspace_bytes(p) bytes, 256-byte aligned, or
+ * NULL for the library's cached allocation - but not while the stream is being
+ * captured, where NULL returns MOE_ERR_WORKSPACE. The second kernel is launched
+ * cooperatively (one CTA per SM, all resident). Calls that may run at the same
+ * time need a workspace each.
  */
 #define MOE_FEW_MAX_TOKENS 16
 size_t moe_few_workspace_bytes(const moe_params* p);
